@@ -1,6 +1,6 @@
 """libmlstm: the xLSTM mLSTM matrix-memory cell on B200 (sm_100a) behind a C ABI.
 
-``binding`` wraps the C entry points of ``include/mlstm.h`` for torch device
+``binding`` wraps the C entry points of the headers in ``include/`` for torch device
 tensors; ``workloads`` draws the seeded synthetic inputs; ``build`` compiles the
 CUDA library in-tree.
 """

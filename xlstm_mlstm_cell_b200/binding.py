@@ -2,7 +2,7 @@
 
 The functions take torch tensors that already live on the GPU, pass their
 device pointers, sizes and the current CUDA stream to the C ABI declared in
-``include/mlstm.h``, and raise ``MlstmError`` on a non-zero status.  Every step
+``include/*.h``, and raise ``MlstmError`` on a non-zero status.  Every step
 of the computation runs in the library's CUDA kernels; there is no other code
 path.  If the library cannot be loaded the import of the functions fails
 loudly (``load()`` raises).
@@ -21,8 +21,14 @@ MLSTM_F32, MLSTM_BF16 = 0, 1
 STATUS = {0: "MLSTM_OK", 1: "MLSTM_ERR_INVALID_ARG", 2: "MLSTM_ERR_UNSUPPORTED", 3: "MLSTM_ERR_WORKSPACE",
           4: "MLSTM_ERR_CUDA", 5: "MLSTM_ERR_TIMEOUT"}
 
-# Every symbol include/mlstm.h and include/slstm.h declare, with its ctypes signature.
-_vp, _fp, _i, _sz = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+
+class _Strides(ctypes.Structure):
+    """qknorm_strides of include/qknorm.h."""
+    _fields_ = [("batch", ctypes.c_longlong), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+# Every symbol the headers under include/ declare, with its ctypes signature.
+_vp, _fp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 SIGNATURES = {
     "mlstm_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "mlstm_fwd": (_i, [_vp, _vp, _vp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _fp, _fp, _fp, _vp, _sz,
@@ -51,6 +57,18 @@ SIGNATURES = {
     "mlstm_selftest_wait_timeout": (_i, [_vp, _vp]),
     "slstm_fwd": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _fp, _fp, _fp, _fp, _vp, _vp, _vp]),
     "slstm_batch_per_cluster": (_i, [_i, _i, _i, _i]),
+    "gdelta_fwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "gdelta_fwd": (_i, [_vp, _vp, _vp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _fp, _vp, _fp, _vp, _sz, _vp]),
+    "gdelta_fwd_tensor_path": (_i, [_i, _i, _i]),
+    "gdelta_step": (_i, [_fp, _vp, _vp, _vp, _fp, _fp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp]),
+    "gdelta_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "gdelta_bwd": (_i, [_vp, _vp, _vp, _fp, _fp, _vp, _fp, _vp, _fp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp,
+                        _fp, _fp, _fp, _vp, _sz, _vp]),
+    "qknorm_fwd": (_i, [_vp, _Strides, _vp, _Strides, _fp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
+                        _vp, _vp]),
+    "qknorm_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "qknorm_bwd": (_i, [_vp, _vp, _vp, _Strides, _vp, _Strides, _fp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                        _i, _vp, _Strides, _vp, _Strides, _fp, _fp, _vp, _sz, _vp]),
 }
 
 _lib = None
@@ -338,3 +356,261 @@ def slstm_fwd(wx, R, forget: str = "exp", state=None, h_out=None, want_h: bool =
 def slstm_batch_per_cluster(B, NH, DH, dtype) -> int:
     dt = MLSTM_BF16 if dtype == torch.bfloat16 else MLSTM_F32
     return int(load().slstm_batch_per_cluster(B, NH, DH, dt))
+
+
+# ---------------------------------------------------------------- gated delta rule
+
+def _need(name, t, shape, dtype, device):
+    """Checks one tensor argument: the C ABI sees only its address."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _need_cuda(t):
+    if t.device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device, got %s" % t.device)
+
+
+class _on:
+    """The device of the arguments as the current one, for the call alone, and the stream to use on it."""
+
+    def __init__(self, device, stream):
+        self.index, self.stream = device.index, stream
+
+    def __enter__(self):
+        self.back = torch.cuda.current_device()
+        if self.back != self.index:
+            torch.cuda.set_device(self.index)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(self.index) if self.stream is None
+                               else self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.back != self.index:
+            torch.cuda.set_device(self.back)
+
+
+def _gdelta_inputs(q, k, v, g, beta, lengths, step=False):
+    """Checks the delta rule's inputs; returns (dt, B, NH, NHV, S, DK, DV)."""
+    dt = _dt(q)
+    _need_cuda(q)
+    if q.dim() != (3 if step else 4) or v.dim() != q.dim():
+        raise ValueError("q, k and v must be %s" % ("[B, heads, D]" if step else "[B, heads, S, D]"))
+    B, NH, *T, DK = q.shape
+    NHV, DV = v.shape[1], v.shape[-1]
+    _need("q", q, q.shape, q.dtype, q.device)
+    _need("k", k, q.shape, q.dtype, q.device)
+    _need("v", v, (B, NHV, *T, DV), q.dtype, q.device)
+    _need("g", g, (B, NHV, *T), torch.float32, q.device)
+    _need("beta", beta, (B, NHV, *T), torch.float32, q.device)
+    if lengths is not None:
+        _need("lengths", lengths, (B,), torch.int32, q.device)
+    return dt, B, NH, NHV, T[0] if T else 1, DK, DV
+
+
+def gdelta_fwd_tensor_path(DK, DV, dtype) -> int:
+    """gdelta_fwd_tensor_path: 1 tensor cores, 0 fp32 on the CUDA cores, -1 unsupported."""
+    return int(load().gdelta_fwd_tensor_path(DK, DV, MLSTM_BF16 if dtype == torch.bfloat16 else MLSTM_F32))
+
+
+def gdelta_workspace_size(B, NH, NHV, S, DK, DV, dtype, backward: bool = False) -> int:
+    """Workspace bytes of gdelta_fwd, or of gdelta_bwd (0: unsupported)."""
+    lib, dt = load(), MLSTM_BF16 if dtype == torch.bfloat16 else MLSTM_F32
+    size = lib.gdelta_bwd_workspace_size if backward else lib.gdelta_fwd_workspace_size
+    return int(size(B, NH, NHV, S, DK, DV, dt))
+
+
+def _gdelta_workspace(workspace, sizes, dt, device, backward):
+    lib = load()
+    fn = "gdelta_bwd_workspace_size" if backward else "gdelta_fwd_workspace_size"
+    if workspace is None:
+        n = int(getattr(lib, fn)(*sizes, dt))
+        if n == 0:
+            raise MlstmError(fn, 2, lib)
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    _need("workspace", workspace, workspace.shape, torch.uint8, device)
+    return workspace
+
+
+def gdelta_fwd(q, k, v, g, beta, state=None, lengths=None, scale=None, o_out=None, state_out=None,
+               return_state: bool = True, workspace=None, stream=None):
+    """gdelta_fwd: the gated delta rule over whole sequences; returns ``(o, final state)``.
+
+    q, k ``[B, NH, S, DK]``, v ``[B, NHV, S, DV]`` (float32 or bfloat16; NHV a multiple of NH), the log
+    forget gates g and the write strengths beta ``[B, NHV, S]`` float32.  ``state`` ``[B, NHV, DK, DV]``
+    float32 is the state to start from (None: zero) and is not changed unless it is ``state_out`` too;
+    ``lengths`` int32 ``[B]`` the real tokens of each item (None: all); ``scale`` defaults to
+    DK ** -0.5.  The state is None with ``return_state=False``.
+    """
+    lib = load()
+    dt, B, NH, NHV, S, DK, DV = _gdelta_inputs(q, k, v, g, beta, lengths)
+    if state is not None:
+        _need("state", state, (B, NHV, DK, DV), torch.float32, q.device)
+    if o_out is None:
+        o_out = torch.empty_like(v)
+    else:
+        _need("o_out", o_out, v.shape, q.dtype, q.device)
+    if state_out is not None:
+        _need("state_out", state_out, (B, NHV, DK, DV), torch.float32, q.device)
+    elif return_state:
+        state_out = torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device)
+    with _on(q.device, stream) as s:
+        workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV), dt, q.device, False)
+        _check("gdelta_fwd", lib.gdelta_fwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(lengths), dt, B, NH, NHV, S, DK, DV,
+            DK ** -0.5 if scale is None else scale, _ptr(state), _ptr(o_out), _ptr(state_out), _ptr(workspace),
+            workspace.numel(), s))
+    return o_out, state_out
+
+
+def gdelta_step(state, q, k, v, g, beta, scale=None, o_out=None, stream=None):
+    """gdelta_step: one token of the gated delta rule; updates ``state`` ``[B, NHV, DK, DV]`` in place
+    and returns o ``[B, NHV, DV]``.  q, k ``[B, NH, DK]``, v ``[B, NHV, DV]``, g, beta ``[B, NHV]``."""
+    lib = load()
+    dt, B, NH, NHV, _, DK, DV = _gdelta_inputs(q, k, v, g, beta, None, step=True)
+    _need("state", state, (B, NHV, DK, DV), torch.float32, q.device)
+    if o_out is None:
+        o_out = torch.empty_like(v)
+    else:
+        _need("o_out", o_out, v.shape, q.dtype, q.device)
+    with _on(q.device, stream) as s:
+        _check("gdelta_step", lib.gdelta_step(
+            _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), dt, B, NH, NHV, DK, DV,
+            DK ** -0.5 if scale is None else scale, _ptr(o_out), s))
+    return o_out
+
+
+def gdelta_bwd(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scale=None, workspace=None, out=None,
+               stream=None):
+    """gdelta_bwd: gradients of ``sum(do * o) + sum(dstate * final state)`` for the forward pass from
+    ``state`` (None: zero; ``dstate`` None: zero).  Returns ``(dq, dk, dv, dg, dbeta, dstate0)``, dstate0
+    None without a ``state``; ``out`` may give those six tensors (the last one or None) to write into."""
+    lib = load()
+    dt, B, NH, NHV, S, DK, DV = _gdelta_inputs(q, k, v, g, beta, lengths)
+    _need("do", do, v.shape, q.dtype, q.device)
+    for name, t in (("state", state), ("dstate", dstate)):
+        if t is not None:
+            _need(name, t, (B, NHV, DK, DV), torch.float32, q.device)
+    if out is None:
+        out = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
+               torch.empty_like(beta), None if state is None else torch.empty_like(state))
+    else:
+        like = (q, k, v, g, beta)
+        for name, t, x in zip(("dq", "dk", "dv", "dg", "dbeta"), out, like):
+            _need(name, t, x.shape, x.dtype, q.device)
+        if out[5] is not None:
+            _need("dstate0", out[5], (B, NHV, DK, DV), torch.float32, q.device)
+    dq, dk, dv, dg, dbeta, dstate0 = out
+    with _on(q.device, stream) as s:
+        workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV), dt, q.device, True)
+        _check("gdelta_bwd", lib.gdelta_bwd(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(lengths), _ptr(state), _ptr(do), _ptr(dstate), dt, B,
+            NH, NHV, S, DK, DV, DK ** -0.5 if scale is None else scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+            _ptr(dbeta), _ptr(dstate0), _ptr(workspace), workspace.numel(), s))
+    return dq, dk, dv, dg, dbeta, dstate0
+
+
+# ---------------------------------------------------------------- norms of queries and keys
+
+QKNORM_KINDS = {"rms": 0, "l2": 1}
+
+
+def _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions):
+    """Checks the norms' inputs; returns (dt, B, S, NHQ, NHK, D, RD, kind)."""
+    dt = _dt(q)
+    _need_cuda(q)
+    if norm not in QKNORM_KINDS:
+        raise ValueError("norm must be one of %s" % ", ".join(map(repr, QKNORM_KINDS)))
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be [B, S, heads, D]")
+    B, S, NHQ, D = q.shape
+    NHK = k.shape[2]
+    if k.shape != (B, S, NHK, D) or k.dtype != q.dtype or k.device != q.device:
+        raise ValueError("k must be [%d, %d, heads, %d] of %s on %s" % (B, S, D, q.dtype, q.device))
+    for name, t in (("q", q), ("k", k)):
+        if t.numel() and t.stride(3) != 1:
+            raise ValueError("the elements of a head of %s must be contiguous" % name)
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _need(name, t, (D,), torch.float32, q.device)
+    RD = 0
+    if inv_freq is not None:
+        RD = 2 * inv_freq.numel()
+        _need("inv_freq", inv_freq, (RD // 2,), torch.float32, q.device)
+        if RD > D:
+            raise ValueError("inv_freq must have at most D / 2 = %d frequencies, got %d" % (D // 2, RD // 2))
+        if positions is not None:
+            _need("positions", positions, (B, S), torch.int32, q.device)
+    elif positions is not None:
+        raise ValueError("positions without inv_freq")
+    return dt, B, S, NHQ, NHK, D, RD, QKNORM_KINDS[norm]
+
+
+def _strides(t):
+    b, s, h, _ = t.stride()
+    return _Strides(b, s, h)
+
+
+def qknorm_fwd(q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: float = 1e-6, inv_freq=None,
+               positions=None, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """qknorm_fwd: norms every head's query and key, weights and rotates them, and lays them out for the
+    cells; returns ``(q_out [B, NHQ, S, D], k_out [B, NHK, S, D])``.
+
+    q ``[B, S, NHQ, D]`` and k ``[B, S, NHK, D]`` (float32 or bfloat16) may be slices of a fused projection:
+    only the last axis has to be contiguous.  norm "rms" divides by sqrt(mean(x^2) + eps), "l2" by
+    sqrt(sum(x^2) + eps); the weights are float32 ``[D]`` or None.  ``inv_freq`` float32 ``[RD / 2]`` rotates the
+    first RD elements by position * inv_freq (None: no rotation); ``positions`` int32 ``[B, S]``, None for
+    0 .. S-1; pairs are (p, p + RD/2), or neighbours with ``interleaved``.
+    """
+    lib = load()
+    dt, B, S, NHQ, NHK, D, RD, kind = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
+    if q_out is None:
+        q_out = torch.empty((B, NHQ, S, D), dtype=q.dtype, device=q.device)
+    else:
+        _need("q_out", q_out, (B, NHQ, S, D), q.dtype, q.device)
+    if k_out is None:
+        k_out = torch.empty((B, NHK, S, D), dtype=q.dtype, device=q.device)
+    else:
+        _need("k_out", k_out, (B, NHK, S, D), q.dtype, q.device)
+    with _on(q.device, stream) as s:
+        _check("qknorm_fwd", lib.qknorm_fwd(
+            _ptr(q), _strides(q), _ptr(k), _strides(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions),
+            dt, B, S, NHQ, NHK, D, RD, kind, eps, 1 if interleaved else 0, _ptr(q_out), _ptr(k_out), s))
+    return q_out, k_out
+
+
+def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: float = 1e-6,
+               inv_freq=None, positions=None, interleaved: bool = False, out=None, workspace=None, stream=None):
+    """qknorm_bwd: the gradients ``(dq, dk, dq_weight, dk_weight)`` of qknorm_fwd's inputs from those of its
+    outputs (weight gradients None where the weight is).  ``out`` may give dq ``[B, S, NHQ, D]`` and dk to
+    write into, such as slices of a fused projection's gradient (views that share no element)."""
+    lib = load()
+    dt, B, S, NHQ, NHK, D, RD, kind = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
+    _need("dq_out", dq_out, (B, NHQ, S, D), q.dtype, q.device)
+    _need("dk_out", dk_out, (B, NHK, S, D), q.dtype, q.device)
+    if out is None:
+        dq = torch.empty((B, S, NHQ, D), dtype=q.dtype, device=q.device)
+        dk = torch.empty((B, S, NHK, D), dtype=q.dtype, device=q.device)
+    else:
+        dq, dk = out
+        for name, t, x in (("dq", dq, q), ("dk", dk, k)):
+            if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or (t.numel() and t.stride(3) != 1):
+                raise ValueError("%s must be like its input, the elements of a head contiguous" % name)
+    dwq = None if q_weight is None else torch.empty_like(q_weight)
+    dwk = None if k_weight is None else torch.empty_like(k_weight)
+    with _on(q.device, stream) as s:
+        if workspace is None:
+            n = int(lib.qknorm_bwd_workspace_size(B, S, NHQ, NHK, D)) if (dwq is not None or dwk is not None) else 0
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        else:
+            _need("workspace", workspace, workspace.shape, torch.uint8, q.device)
+        _check("qknorm_bwd", lib.qknorm_bwd(
+            _ptr(dq_out), _ptr(dk_out), _ptr(q), _strides(q), _ptr(k), _strides(k), _ptr(q_weight), _ptr(k_weight),
+            _ptr(inv_freq), _ptr(positions), dt, B, S, NHQ, NHK, D, RD, kind, eps, 1 if interleaved else 0, _ptr(dq),
+            _strides(dq), _ptr(dk), _strides(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace), workspace.numel(), s))
+    return dq, dk, dwq, dwk

@@ -1,0 +1,732 @@
+// gdelta_simt.cu -- the gated delta rule chunk by chunk on the CUDA cores in fp32: the path of fp32
+// inputs and of every shape the tensor-core kernels do not take.
+//
+// With a the cumulative log gates of a chunk, D_ij = exp(a_i - a_j), S the state at its start:
+//   prep     KK = strict_lower(D * K K^T), P = lower(D * Q K^T), T = (I + KK diag(beta))^-1
+//   walk     Y = V - e^a K S,  E = T Y,  U = beta E,  O = scale (e^a Q S + P U),
+//            S' = e^{a_64} S + K^T (e^{a_64 - a} U)
+//   reverse  dU = scale P^T dO + e^{a_64 - a} K dS',  dV = T^T (beta dU),
+//            dS = e^{a_64} dS' + scale Q^T (e^a dO) - K^T (e^a dV)
+//   grad     H = dV E^T,  dP = scale (dO E^T) diag(beta),  dA = -H diag(beta),
+//            Zq = scale e^a dO S^T,  Zk = -e^a dV S^T,  W = e^{a_64 - a} U dS'^T,
+//            dQ = Zq + (dP * D) K,  dK = Zk + W + (dP * D)^T Q + (dA * D + (dA * D)^T) K,
+//            dbeta_j = E_j . dU_j - sum_i KK_ij H_ij,
+//            dg_t = sum_{i >= t} (Zq . Q + Zk . K)_i + sum_{j < t} (W . K)_j
+//                   + sum_{j < t <= i} (dP * P + dA * KK)_ij + e^{a_64} <S, dS'>
+// (dP * D masked to j <= i, dA * D to j < i.)  Only the walks are sequential over the chunks; their
+// work splits over value columns, 32 to a CTA.  Products are register tiles of 4 x 4 or 8 x 8 fed by
+// 16-byte shared-memory loads with the reduction index outermost; what bounds these kernels is the
+// CUDA cores' fp32 rate and, for few heads, the chain of three products per chunk.
+#include "gdelta_prep.cuh"
+
+#include <algorithm>
+
+namespace mlstm {
+namespace gdelta {
+namespace {
+
+constexpr int LDR = 132;   // row stride of [.][128] tiles
+constexpr int VT = 32;     // value columns of a walk CTA
+
+MLSTM_DEVINL float4 ld4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+MLSTM_DEVINL void st4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+
+// Rows r < 64 of src (row stride DK, `len` of them live) into columns c0 + r of dst [DK][LDR].
+template <typename T>
+MLSTM_DEVINL void stage_transposed(const T *src, int len, int DK, float *dst, int c0, int tid, int nthr)
+{
+    for (int i = tid; i < 64 * (DK / 4); i += nthr) {
+        const int r = i & 63, d = (i >> 6) * 4;
+        const float4 x = r < len ? load4(src + (size_t)r * DK + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        dst[(d + 0) * LDR + c0 + r] = x.x;
+        dst[(d + 1) * LDR + c0 + r] = x.y;
+        dst[(d + 2) * LDR + c0 + r] = x.z;
+        dst[(d + 3) * LDR + c0 + r] = x.w;
+    }
+}
+
+MLSTM_DEVINL void fma4x4(float (&acc)[4][4], float4 a, float4 b)
+{
+    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+}
+
+// ---------------------------------------------------------------- prep
+
+constexpr size_t PREP_SMEM = sizeof(float) * (128 * LDR + 64 * LDT + 32 * 33 + 64) + sizeof(float2) * 64;
+
+// One CTA per chunk and key head: K K^T and Q K^T once, then the matrices of every value head on it.
+template <typename T>
+__global__ void __launch_bounds__(256, 2)
+prep_kernel(const T *__restrict__ q, const T *__restrict__ k, const float *__restrict__ g,
+            const float *__restrict__ beta, const int *__restrict__ lengths, int NH, int NHV, int S, int DK,
+            Workspace w, bool want_kk)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *kq = sm;                       // [DK][LDR]: K in columns 0..63, Q in 64..127
+    float *m = kq + 128 * LDR;            // [64][LDT]
+    float *tmp = m + 64 * LDT;
+    float *bt = tmp + 32 * 33;            // [64]
+    float2 *a = reinterpret_cast<float2 *>(bt + 64);
+    const int tid = threadIdx.x, c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (c == 0 && bh == 0 && tid == 0) *w.status = 0u;
+    const int len = min(CH, live_tokens(lengths, b, S) - c * CH);
+    if (len <= 0) return;
+    const size_t row0 = (size_t)bh * S + c * CH;
+    stage_transposed(k + row0 * DK, len, DK, kq, 0, tid, 256);
+    stage_transposed(q + row0 * DK, len, DK, kq, 64, tid, 256);
+    __syncthreads();
+    const int i0 = (tid >> 4) * 4, j0 = (tid & 15) * 4;
+    float kk[4][4] = {}, qk[4][4] = {};
+    for (int d = 0; d < DK; ++d) {
+        const float4 y = ld4(kq + d * LDR + j0);
+        fma4x4(kk, ld4(kq + d * LDR + i0), y);
+        fma4x4(qk, ld4(kq + d * LDR + 64 + i0), y);
+    }
+    for (int h = 0; h < group; ++h) {
+        const int bhv = b * NHV + (bh % NH) * group + h;
+        const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
+        __syncthreads();
+        if (tid < 32) chunk_gates(g + gt, len, tid, a);
+        else if (tid < 96) bt[tid - 32] = tid - 32 < len ? beta[gt + tid - 32] : 0.f;
+        __syncthreads();
+        if (tid < 64) w.A[ch * 64 + tid] = a[tid];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = i0 + r;
+            float p[4], x[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int j = j0 + s;
+                const float dec = j <= i ? expf(gate_diff(a[i], a[j])) : 0.f;
+                p[s] = j <= i ? dec * qk[r][s] : 0.f;
+                x[s] = j < i ? dec * kk[r][s] : 0.f;
+                m[i * LDT + j] = x[s] * bt[j];
+            }
+            st4(w.P + ch * 4096 + i * 64 + j0, make_float4(p[0], p[1], p[2], p[3]));
+            if (want_kk) st4(w.KK + ch * 4096 + i * 64 + j0, make_float4(x[0], x[1], x[2], x[3]));
+        }
+        __syncthreads();
+        invert64(m, tmp, tid, 256, [] { __syncthreads(); });
+        for (int i = tid; i < 64 * 16; i += 256)
+            st4(w.T + ch * 4096 + (i >> 4) * 64 + (i & 15) * 4, ld4(m + (i >> 4) * LDT + (i & 15) * 4));
+    }
+}
+
+// ---------------------------------------------------------------- forward walk
+
+constexpr size_t WALK_SMEM = sizeof(float) * (128 * LDR + 128 * VT + 2 * 64 * LDT + 64 * VT + 3 * 64);
+
+// One CTA per value head and 32 value columns; KEEP: the backward's recomputation (writes the states at
+// the chunks' starts and E, no outputs).
+template <typename T, bool KEEP>
+__global__ void __launch_bounds__(256)
+walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+            const float *__restrict__ beta, const int *__restrict__ lengths, const float *S0, int NH, int NHV,
+            int S, int DK, int DV, float scale, Workspace w, T *__restrict__ o, float *S_final)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *kq = sm;                    // [DK][LDR]
+    float *st = kq + 128 * LDR;        // [DK][VT] the state
+    float *tt = st + 128 * VT;         // [64][LDT] T transposed
+    float *pt = tt + 64 * LDT;         // [64][LDT] P transposed
+    float *y = pt + 64 * LDT;          // [64][VT] Y, then U, then e^{a_64 - a} U
+    float *ea = y + 64 * VT, *eo = ea + 64, *bt = eo + 64;
+    const int tid = threadIdx.x, c0 = blockIdx.x * VT, bhv = blockIdx.y, b = bhv / NHV;
+    const int bh = b * NH + (bhv % NHV) / (NHV / NH);
+    const int r0 = (tid >> 3) * 4, j0 = (tid & 7) * 4, col = c0 + j0;   // the thread's tile of 4 x 4
+    const bool in = col < DV, krow = r0 < 64;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int n = live_tokens(lengths, b, S);
+    for (int i = tid; i < DK * 8; i += 256) {
+        const int d = i >> 3, j = (i & 7) * 4;
+        st4(st + d * VT + j, S0 && c0 + j < DV ? ld4(S0 + ((size_t)bhv * DK + d) * DV + c0 + j)
+                                               : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    for (int c = 0; c * CH < n; ++c) {
+        const int len = min(CH, n - c * CH);
+        const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * S + c * CH;
+        __syncthreads();
+        stage_transposed(k + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 0, tid, 256);
+        if (!KEEP) stage_transposed(q + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 64, tid, 256);
+        for (int i = tid; i < 64 * 16; i += 256) {
+            const int r = i & 63, j = (i >> 6) * 4;
+            float4 x = ld4(w.T + ch * 4096 + r * 64 + j);
+            tt[(j + 0) * LDT + r] = x.x; tt[(j + 1) * LDT + r] = x.y;
+            tt[(j + 2) * LDT + r] = x.z; tt[(j + 3) * LDT + r] = x.w;
+            if (!KEEP) {
+                x = ld4(w.P + ch * 4096 + r * 64 + j);
+                pt[(j + 0) * LDT + r] = x.x; pt[(j + 1) * LDT + r] = x.y;
+                pt[(j + 2) * LDT + r] = x.z; pt[(j + 3) * LDT + r] = x.w;
+            }
+        }
+        if (tid < 64) {
+            const float2 x = w.A[ch * 64 + tid];
+            ea[tid] = expf(x.x + x.y);
+            eo[tid] = expf(gate_diff(w.A[ch * 64 + 63], x));
+            bt[tid] = tid < len ? beta[vrow + tid] : 0.f;
+        }
+        __syncthreads();
+        if (KEEP)
+            for (int i = tid; i < DK * 8; i += 256) {
+                const int d = i >> 3, j = (i & 7) * 4;
+                if (c0 + j < DV) st4(w.SC + (ch * DK + d) * DV + c0 + j, ld4(st + d * VT + j));
+            }
+        float acc[4][4] = {};   // K S (rows 0..63) and Q S (rows 64..127)
+        if (krow || !KEEP)
+            for (int d = 0; d < DK; ++d) fma4x4(acc, ld4(kq + d * LDR + r0), ld4(st + d * VT + j0));
+        if (krow) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = r0 + r;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t < len && in) {
+                    x = load4(v + (vrow + t) * DV + col);
+                    x.x -= ea[t] * acc[r][0]; x.y -= ea[t] * acc[r][1];
+                    x.z -= ea[t] * acc[r][2]; x.w -= ea[t] * acc[r][3];
+                }
+                st4(y + t * VT + j0, x);
+            }
+        }
+        __syncthreads();
+        float e[4][4] = {};
+        if (krow)
+            for (int j = 0; j < r0 + 4; ++j) fma4x4(e, ld4(tt + j * LDT + r0), ld4(y + j * VT + j0));
+        __syncthreads();
+        if (krow) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = r0 + r;
+                if (KEEP && in) st4(w.E + (ch * 64 + t) * DV + col, make_float4(e[r][0], e[r][1], e[r][2], e[r][3]));
+                const float f = KEEP ? bt[t] * eo[t] : bt[t];
+                st4(y + t * VT + j0, make_float4(f * e[r][0], f * e[r][1], f * e[r][2], f * e[r][3]));
+            }
+        }
+        __syncthreads();
+        if (!KEEP) {
+            if (!krow) {
+                float s[4][4] = {};
+                for (int j = 0; j < r0 - 60; ++j) fma4x4(s, ld4(pt + j * LDT + r0 - 64), ld4(y + j * VT + j0));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = r0 - 64 + r;
+                    if (t < len && in)
+                        store4(o + (vrow + t) * DV + col,
+                               make_float4(scale * (ea[t] * acc[r][0] + s[r][0]), scale * (ea[t] * acc[r][1] + s[r][1]),
+                                           scale * (ea[t] * acc[r][2] + s[r][2]), scale * (ea[t] * acc[r][3] + s[r][3])));
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < 64 * 8; i += 256) {
+                float4 x = ld4(y + i * 4);
+                const float f = eo[i >> 3];
+                st4(y + i * 4, make_float4(f * x.x, f * x.y, f * x.z, f * x.w));
+            }
+            __syncthreads();
+        }
+        if (r0 < DK) {   // S' rows r0 .. r0 + 3 (DK is a multiple of 8)
+            float s[4][4];
+            const float f = ea[63];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 x = ld4(st + (r0 + r) * VT + j0);
+                s[r][0] = f * x.x; s[r][1] = f * x.y; s[r][2] = f * x.z; s[r][3] = f * x.w;
+            }
+            for (int j = 0; j < 64; j += 4) {
+                float4 kr[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kr[r] = ld4(kq + (r0 + r) * LDR + j);
+                fma4x4(s, make_float4(kr[0].x, kr[1].x, kr[2].x, kr[3].x), ld4(y + j * VT + j0));
+                fma4x4(s, make_float4(kr[0].y, kr[1].y, kr[2].y, kr[3].y), ld4(y + (j + 1) * VT + j0));
+                fma4x4(s, make_float4(kr[0].z, kr[1].z, kr[2].z, kr[3].z), ld4(y + (j + 2) * VT + j0));
+                fma4x4(s, make_float4(kr[0].w, kr[1].w, kr[2].w, kr[3].w), ld4(y + (j + 3) * VT + j0));
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st4(st + (r0 + r) * VT + j0, make_float4(s[r][0], s[r][1], s[r][2], s[r][3]));
+        }
+    }
+    if (KEEP) return;
+    __syncthreads();
+    for (int i = tid; i < (S - n) * 8; i += 256) {   // padding
+        const int j = c0 + (i & 7) * 4;
+        if (j < DV) store4(o + ((size_t)bhv * S + n + (i >> 3)) * DV + j, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    if (S_final)
+        for (int i = tid; i < DK * 8; i += 256) {
+            const int d = i >> 3, j = (i & 7) * 4;
+            if (c0 + j < DV) st4(S_final + ((size_t)bhv * DK + d) * DV + c0 + j, ld4(st + d * VT + j));
+        }
+}
+
+// ---------------------------------------------------------------- reverse walk
+
+constexpr size_t REV_SMEM = sizeof(float) * (128 * LDR + 128 * VT + 2 * 64 * LDT + 3 * 64 * VT + 3 * 64);
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+reverse_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ d_o,
+               const float *__restrict__ beta, const int *__restrict__ lengths, const float *dS_final, int NH,
+               int NHV, int S, int DK, int DV, float scale, Workspace w, T *__restrict__ dv, float *dS0)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *kq = sm;                    // [DK][LDR]
+    float *ds = kq + 128 * LDR;        // [DK][VT] the state's gradient
+    float *tm = ds + 128 * VT;         // [64][LDT] T
+    float *pm = tm + 64 * LDT;         // [64][LDT] P
+    float *dob = pm + 64 * LDT;        // [64][VT] dO, then scale e^a dO
+    float *x = dob + 64 * VT;          // [64][VT] P^T dO, then -e^a dV
+    float *y = x + 64 * VT;            // [64][VT] beta dU
+    float *ea = y + 64 * VT, *eo = ea + 64, *bt = eo + 64;
+    const int tid = threadIdx.x, c0 = blockIdx.x * VT, bhv = blockIdx.y, b = bhv / NHV;
+    const int bh = b * NH + (bhv % NHV) / (NHV / NH);
+    const int r0 = (tid >> 3) * 4, j0 = (tid & 7) * 4, col = c0 + j0;
+    const bool in = col < DV, krow = r0 < 64;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int n = live_tokens(lengths, b, S);
+    for (int i = tid; i < DK * 8; i += 256) {
+        const int d = i >> 3, j = (i & 7) * 4;
+        st4(ds + d * VT + j, dS_final && c0 + j < DV ? ld4(dS_final + ((size_t)bhv * DK + d) * DV + c0 + j)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    for (int c = (n + CH - 1) / CH - 1; c >= 0; --c) {
+        const int len = min(CH, n - c * CH);
+        const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * S + c * CH;
+        __syncthreads();
+        stage_transposed(k + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 0, tid, 256);
+        stage_transposed(q + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 64, tid, 256);
+        for (int i = tid; i < 64 * 16; i += 256) {
+            const int r = i >> 4, j = (i & 15) * 4;
+            st4(tm + r * LDT + j, ld4(w.T + ch * 4096 + r * 64 + j));
+            st4(pm + r * LDT + j, ld4(w.P + ch * 4096 + r * 64 + j));
+        }
+        for (int i = tid; i < 64 * 8; i += 256) {
+            const int t = i >> 3, j = (i & 7) * 4;
+            st4(dob + t * VT + j, t < len && c0 + j < DV ? load4(d_o + (vrow + t) * DV + c0 + j)
+                                                         : make_float4(0.f, 0.f, 0.f, 0.f));
+        }
+        if (tid < 64) {
+            const float2 z = w.A[ch * 64 + tid];
+            ea[tid] = expf(z.x + z.y);
+            eo[tid] = expf(gate_diff(w.A[ch * 64 + 63], z));
+            bt[tid] = tid < len ? beta[vrow + tid] : 0.f;
+        }
+        __syncthreads();
+        for (int i = tid; i < DK * 8; i += 256) {
+            const int d = i >> 3, j = (i & 7) * 4;
+            if (c0 + j < DV) st4(w.DSC + (ch * DK + d) * DV + c0 + j, ld4(ds + d * VT + j));
+        }
+        float acc[4][4] = {};   // rows 0..63: K dS'; rows 64..127: P^T dO
+        if (krow) {
+            for (int d = 0; d < DK; ++d) fma4x4(acc, ld4(kq + d * LDR + r0), ld4(ds + d * VT + j0));
+        } else {
+            for (int i = r0 - 64; i < 64; ++i) fma4x4(acc, ld4(pm + i * LDT + r0 - 64), ld4(dob + i * VT + j0));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                st4(x + (r0 - 64 + r) * VT + j0, make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]));
+        }
+        __syncthreads();
+        if (krow) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = r0 + r;
+                float4 p = ld4(x + t * VT + j0);
+                p.x = scale * p.x + eo[t] * acc[r][0]; p.y = scale * p.y + eo[t] * acc[r][1];
+                p.z = scale * p.z + eo[t] * acc[r][2]; p.w = scale * p.w + eo[t] * acc[r][3];
+                if (in) st4(w.DU + (ch * 64 + t) * DV + col, p);
+                st4(y + t * VT + j0, make_float4(bt[t] * p.x, bt[t] * p.y, bt[t] * p.z, bt[t] * p.w));
+            }
+        }
+        __syncthreads();
+        if (krow) {
+            float e[4][4] = {};
+            for (int i = r0; i < 64; ++i) fma4x4(e, ld4(tm + i * LDT + r0), ld4(y + i * VT + j0));
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = r0 + r;
+                const float4 p = make_float4(e[r][0], e[r][1], e[r][2], e[r][3]);
+                if (in) {
+                    st4(w.DV + (ch * 64 + t) * DV + col, p);
+                    if (t < len) store4(dv + (vrow + t) * DV + col, p);
+                }
+                const float f = t < len ? -ea[t] : 0.f;
+                st4(x + t * VT + j0, make_float4(f * p.x, f * p.y, f * p.z, f * p.w));
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {   // dO is no longer read
+                const int t = r0 - 64 + r;
+                float4 p = ld4(dob + t * VT + j0);
+                const float f = scale * ea[t];
+                st4(dob + t * VT + j0, make_float4(f * p.x, f * p.y, f * p.z, f * p.w));
+            }
+        }
+        __syncthreads();
+        if (r0 < DK) {
+            float s[4][4];
+            const float f = ea[63];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float4 p = ld4(ds + (r0 + r) * VT + j0);
+                s[r][0] = f * p.x; s[r][1] = f * p.y; s[r][2] = f * p.z; s[r][3] = f * p.w;
+            }
+            for (int j = 0; j < 128; j += 4) {
+                const float *z = j < 64 ? x + j * VT + j0 : dob + (j - 64) * VT + j0;   // K with -e^a dV, Q with scale e^a dO
+                float4 kr[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) kr[r] = ld4(kq + (r0 + r) * LDR + j);
+                fma4x4(s, make_float4(kr[0].x, kr[1].x, kr[2].x, kr[3].x), ld4(z));
+                fma4x4(s, make_float4(kr[0].y, kr[1].y, kr[2].y, kr[3].y), ld4(z + VT));
+                fma4x4(s, make_float4(kr[0].z, kr[1].z, kr[2].z, kr[3].z), ld4(z + 2 * VT));
+                fma4x4(s, make_float4(kr[0].w, kr[1].w, kr[2].w, kr[3].w), ld4(z + 3 * VT));
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st4(ds + (r0 + r) * VT + j0, make_float4(s[r][0], s[r][1], s[r][2], s[r][3]));
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < (S - n) * 8; i += 256) {
+        const int j = c0 + (i & 7) * 4;
+        if (j < DV) store4(dv + ((size_t)bhv * S + n + (i >> 3)) * DV + j, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    if (dS0)
+        for (int i = tid; i < DK * 8; i += 256) {
+            const int d = i >> 3, j = (i & 7) * 4;
+            if (c0 + j < DV) st4(dS0 + ((size_t)bhv * DK + d) * DV + c0 + j, ld4(ds + d * VT + j));
+        }
+}
+
+// ---------------------------------------------------------------- gradients of a chunk
+
+constexpr int LDK = 132;   // row stride of K and Q [64][128]
+constexpr size_t GRAD_SMEM =
+    sizeof(float) * (2 * 64 * LDK + 2 * 64 * LDT + 32 * (LDR + LDT + LDR + LDR) + 10 * 64 + 32) + sizeof(float2) * 64;
+
+// The thread's 8 x 8 tile of a product with 128 columns: rows ra + {0..3}, rb + {0..3}, columns
+// 4 (tid & 15) + {0..3} and 64 more.
+MLSTM_DEVINL void fma8x8(float (&acc)[8][8], float4 a0, float4 a1, float4 b0, float4 b1)
+{
+    const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+    const float bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+}
+
+MLSTM_DEVINL float half_warp_sum(float x)
+{
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// One CTA per chunk and key head, over the value heads on it; dq and dk stay in registers.
+template <typename T>
+__global__ void __launch_bounds__(256, 1)
+grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ d_o,
+            const float *__restrict__ beta, const int *__restrict__ lengths, int NH, int NHV, int S, int DK, int DV,
+            float scale, Workspace w, T *__restrict__ dq, T *__restrict__ dk, float *__restrict__ dg,
+            float *__restrict__ dbeta)
+{
+    extern __shared__ __align__(16) float sm[];
+    float *ks = sm, *qs = ks + 64 * LDK;          // [64][LDK] K, Q, columns behind DK zero
+    float *mp = qs + 64 * LDK, *ma = mp + 64 * LDT;   // [64][LDT] dP * D, dA * D
+    float *ta = ma + 64 * LDT;                    // [32][LDR] value block: dO in 0..63, dV in 64..127
+    float *te = ta + 32 * LDR;                    // [32][LDT] E
+    float *ts = te + 32 * LDT;                    // [32][LDR] S transposed
+    float *td = ts + 32 * LDR;                    // [32][LDR] dS' transposed
+    float *ea = td + 32 * LDR, *eo = ea + 64, *bt = eo + 64, *zin = bt + 64, *zout = zin + 64;
+    float *red = zout + 64;                       // [4][64] + [32]
+    float *ssum = red + 256;
+    float *eu = ssum + 32;                        // [64] E . dU
+    float2 *a = reinterpret_cast<float2 *>(eu + 64);
+    const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
+    const int ty = tid >> 4, tx = tid & 15;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int full = min(CH, S - c * CH);
+    const int len = min(full, live_tokens(lengths, b, S) - c * CH);
+    const size_t row0 = (size_t)bh * S + c * CH;
+    const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int first = max(len, 0);
+    for (int i = tid; i < (full - first) * (DK / 4); i += 256) {   // padding
+        const size_t at = (row0 + first) * DK + (size_t)i * 4;
+        store4(dq + at, zero4);
+        store4(dk + at, zero4);
+    }
+    for (int h = 0; h < group; ++h)
+        if (tid < full - first) {
+            const size_t gt = (size_t)(b * NHV + (bh % NH) * group + h) * S + c * CH + first + tid;
+            dg[gt] = 0.f;
+            dbeta[gt] = 0.f;
+        }
+    if (len <= 0) return;
+    for (int i = tid; i < 64 * 32; i += 256) {
+        const int r = i >> 5, d = (i & 31) * 4;
+        const bool ok = r < len && d < DK;
+        st4(ks + r * LDK + d, ok ? load4(k + (row0 + r) * DK + d) : zero4);
+        st4(qs + r * LDK + d, ok ? load4(q + (row0 + r) * DK + d) : zero4);
+    }
+    float acc[8][8] = {};   // rows 4 ty + {0..3} of dq, and of dk
+    for (int h = 0; h < group; ++h) {
+        const int bhv = b * NHV + (bh % NH) * group + h;
+        const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * S + c * CH;
+        __syncthreads();
+        if (tid < 64) {
+            const float2 x = w.A[ch * 64 + tid];
+            a[tid] = x;
+            ea[tid] = expf(x.x + x.y);
+            eo[tid] = expf(gate_diff(w.A[ch * 64 + 63], x));
+            bt[tid] = tid < len ? beta[vrow + tid] : 0.f;
+        }
+        __syncthreads();
+        // H = dV E^T and dO E^T (64 x 64 each), then Z = [dO; dV] S^T and W = E dS'^T
+        float hx[8][4] = {}, z[8][8] = {}, wv[4][8] = {};
+        float sd = 0.f, euv = 0.f;
+        for (int v0 = 0; v0 < DV; v0 += 32) {
+            for (int i = tid; i < 64 * 8; i += 256) {
+                const int t = i & 63, j = (i >> 6) * 4;
+                const bool ok = v0 + j < DV && t < len;
+                const float4 x = ok ? load4(d_o + (vrow + t) * DV + v0 + j) : zero4;
+                const float4 y = ok ? ld4(w.DV + (ch * 64 + t) * DV + v0 + j) : zero4;
+                const float4 e = ok ? ld4(w.E + (ch * 64 + t) * DV + v0 + j) : zero4;
+                const float4 u = ok ? ld4(w.DU + (ch * 64 + t) * DV + v0 + j) : zero4;
+                euv += e.x * u.x + e.y * u.y + e.z * u.z + e.w * u.w;   // t is the same in every round
+                const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, es[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    ta[(j + r) * LDR + t] = xs[r];
+                    ta[(j + r) * LDR + 64 + t] = ys[r];
+                    te[(j + r) * LDT + t] = es[r];
+                }
+            }
+            for (int i = tid; i < 128 * 8; i += 256) {
+                const int d = i & 127, j = (i >> 7) * 4;
+                const bool ok = d < DK && v0 + j < DV;
+                const float4 x = ok ? ld4(w.SC + (ch * DK + d) * DV + v0 + j) : zero4;
+                const float4 y = ok ? ld4(w.DSC + (ch * DK + d) * DV + v0 + j) : zero4;
+                sd += x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
+                ts[(j + 0) * LDR + d] = x.x; ts[(j + 1) * LDR + d] = x.y; ts[(j + 2) * LDR + d] = x.z; ts[(j + 3) * LDR + d] = x.w;
+                td[(j + 0) * LDR + d] = y.x; td[(j + 1) * LDR + d] = y.y; td[(j + 2) * LDR + d] = y.z; td[(j + 3) * LDR + d] = y.w;
+            }
+            __syncthreads();
+            for (int l = 0; l < 32; ++l) {
+                const float4 x0 = ld4(ta + l * LDR + 4 * ty), x1 = ld4(ta + l * LDR + 64 + 4 * ty);
+                const float4 s0 = ld4(ts + l * LDR + 4 * tx), s1 = ld4(ts + l * LDR + 64 + 4 * tx);
+                fma8x8(z, x0, x1, s0, s1);
+                const float4 e0 = ld4(te + l * LDT + 4 * tx);
+                const float xv[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+                const float ev[4] = {e0.x, e0.y, e0.z, e0.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) hx[i][j] = fmaf(xv[i], ev[j], hx[i][j]);
+                const float4 er = ld4(te + l * LDT + 4 * ty);
+                const float4 d0 = ld4(td + l * LDR + 4 * tx), d1 = ld4(td + l * LDR + 64 + 4 * tx);
+                const float rv[4] = {er.x, er.y, er.z, er.w};
+                const float dv[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) wv[i][j] = fmaf(rv[i], dv[j], wv[i][j]);
+            }
+            __syncthreads();
+        }
+        red[(tid >> 6) * 64 + (tid & 63)] = euv;
+        sd = warp_sum(sd);
+        if (lane == 0) ssum[tid >> 5] = sd;
+        // the inter-chunk terms of dq and dk, and their products with q and k
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int t = 4 * ty + r;
+            const float fq = scale * ea[t], fk = -ea[t], fw = eo[t] * bt[t];
+            float zi = 0.f, zo = 0.f;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) {
+                const int d = s < 4 ? 4 * tx + s : 60 + 4 * tx + s;
+                const float x = fq * z[r][s], y = fk * z[4 + r][s], u = fw * wv[r][s];
+                acc[r][s] += x;
+                acc[4 + r][s] += y + u;
+                zi += x * qs[t * LDK + d] + y * ks[t * LDK + d];
+                zo += u * ks[t * LDK + d];
+            }
+            zi = half_warp_sum(zi);
+            zo = half_warp_sum(zo);
+            if (tx == 0) { zin[t] = zi; zout[t] = zo; }
+        }
+        // dP * D and dA * D to mp and ma; first the pairs' shares of the gates' and of beta's gradients
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * ty + r;
+            const float4 p4 = ld4(w.P + ch * 4096 + i * 64 + 4 * tx), k4 = ld4(w.KK + ch * 4096 + i * 64 + 4 * tx);
+            const float pv[4] = {p4.x, p4.y, p4.z, p4.w}, kv[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int j = 4 * tx + s;
+                mp[i * LDT + j] = j < i ? bt[j] * (scale * hx[r][s] * pv[s] - hx[4 + r][s] * kv[s]) : 0.f;
+                ma[i * LDT + j] = j < i ? kv[s] * hx[4 + r][s] : 0.f;
+            }
+        }
+        __syncthreads();
+        if (tid < 64) {   // row i: the sums over j < t
+            float s = 0.f;
+            for (int j = 0; j < 64; ++j) {
+                const float x = mp[tid * LDT + j];
+                mp[tid * LDT + j] = s;
+                s += x;
+            }
+        } else if (tid < 128) {   // column j of KK * H
+            const int j = tid - 64;
+            float s = 0.f;
+            for (int i = j + 1; i < 64; ++i) s += ma[i * LDT + j];
+            if (j < len) dbeta[vrow + j] = red[j] + red[64 + j] + red[128 + j] + red[192 + j] - s;
+        }
+        __syncthreads();
+        if (tid < len) {
+            const int t = tid;
+            float s = 0.f;
+            for (int i = t; i < 64; ++i) s += mp[i * LDT + t] + zin[i];
+            for (int j = 0; j < t; ++j) s += zout[j];
+            float sdd = 0.f;
+            for (int i = 0; i < 8; ++i) sdd += ssum[i];
+            dg[vrow + t] = s + ea[63] * sdd;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 4 * ty + r;
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int j = 4 * tx + s;
+                const float dec = j <= i ? bt[j] * expf(gate_diff(a[i], a[j])) : 0.f;
+                mp[i * LDT + j] = j <= i ? scale * dec * hx[r][s] : 0.f;
+                ma[i * LDT + j] = j < i ? -dec * hx[4 + r][s] : 0.f;
+            }
+        }
+        __syncthreads();
+        // dq_i += sum_j mp_ij k_j;  dk_i += sum_j mp_ji q_j + (ma_ij + ma_ji) k_j
+        for (int j = 0; j < 64; ++j) {
+            const float4 k0 = ld4(ks + j * LDK + 4 * tx), k1 = ld4(ks + j * LDK + 64 + 4 * tx);
+            const float4 q0 = ld4(qs + j * LDK + 4 * tx), q1 = ld4(qs + j * LDK + 64 + 4 * tx);
+            const float4 pj = ld4(mp + j * LDT + 4 * ty), aj = ld4(ma + j * LDT + 4 * ty);
+            const float pr[4] = {pj.x, pj.y, pj.z, pj.w}, ar[4] = {aj.x, aj.y, aj.z, aj.w};
+            const float kv[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+            const float qv[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 4 * ty + r;
+                const float x = mp[i * LDT + j], y = ma[i * LDT + j] + ar[r];
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    acc[r][s] = fmaf(x, kv[s], acc[r][s]);
+                    acc[4 + r][s] = fmaf(pr[r], qv[s], fmaf(y, kv[s], acc[4 + r][s]));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int t = 4 * ty + r;
+        if (t >= len) continue;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int d = 64 * s + 4 * tx;
+            if (d >= DK) continue;
+            store4(dq + (row0 + t) * DK + d, make_float4(acc[r][4 * s], acc[r][4 * s + 1], acc[r][4 * s + 2], acc[r][4 * s + 3]));
+            store4(dk + (row0 + t) * DK + d,
+                   make_float4(acc[4 + r][4 * s], acc[4 + r][4 * s + 1], acc[4 + r][4 * s + 2], acc[4 + r][4 * s + 3]));
+        }
+    }
+}
+
+__global__ void state_copy_kernel(const float *S0, float *S_final, size_t n)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    for (size_t i = blockIdx.x * (size_t)blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
+        S_final[i] = S0 ? S0[i] : 0.f;
+}
+
+template <typename K>
+cudaError_t smem_limit(K kernel, size_t bytes)
+{
+    return ensure_dynamic_smem((const void *)kernel, (int)bytes);
+}
+
+template <typename T>
+cudaError_t prep_t(const Args &a, const Workspace &w, bool kk)
+{
+    cudaError_t e = smem_limit(prep_kernel<T>, PREP_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(prep_kernel<T>, dim3(w.NC, a.B * a.NH), dim3(256), PREP_SMEM, a.stream, 1, (const T *)a.q,
+                         (const T *)a.k, a.g, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, w, kk);
+}
+
+template <typename T, bool KEEP>
+cudaError_t walk_t(const Args &a, const Workspace &w, void *o, float *S_final)
+{
+    cudaError_t e = smem_limit(walk_kernel<T, KEEP>, WALK_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(walk_kernel<T, KEEP>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(256), WALK_SMEM, a.stream, 1,
+                         (const T *)a.q, (const T *)a.k, (const T *)a.v, a.beta, a.lengths, a.S0, a.NH, a.NHV, a.S,
+                         a.DK, a.DV, a.scale, w, (T *)o, S_final);
+}
+
+template <typename T>
+cudaError_t reverse_t(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv, float *dS0)
+{
+    cudaError_t e = smem_limit(reverse_kernel<T>, REV_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(reverse_kernel<T>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(256), REV_SMEM, a.stream, 1,
+                         (const T *)a.q, (const T *)a.k, (const T *)d_o, a.beta, a.lengths, dS_final, a.NH, a.NHV, a.S,
+                         a.DK, a.DV, a.scale, w, (T *)dv, dS0);
+}
+
+template <typename T>
+cudaError_t grad_t(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg, float *dbeta)
+{
+    cudaError_t e = smem_limit(grad_kernel<T>, GRAD_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(grad_kernel<T>, dim3(w.NC, a.B * a.NH), dim3(256), GRAD_SMEM, a.stream, 1, (const T *)a.q,
+                         (const T *)a.k, (const T *)d_o, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w,
+                         (T *)dq, (T *)dk, dg, dbeta);
+}
+
+}  // namespace
+
+cudaError_t launch_prep(const Args &a, const Workspace &w, bool kk)
+{
+    return a.bf16 ? prep_t<__nv_bfloat16>(a, w, kk) : prep_t<float>(a, w, kk);
+}
+
+cudaError_t launch_walk(const Args &a, const Workspace &w, void *o, float *S_final, bool keep)
+{
+    if (a.bf16) return keep ? walk_t<__nv_bfloat16, true>(a, w, o, S_final) : walk_t<__nv_bfloat16, false>(a, w, o, S_final);
+    return keep ? walk_t<float, true>(a, w, o, S_final) : walk_t<float, false>(a, w, o, S_final);
+}
+
+cudaError_t launch_reverse(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv, float *dS0)
+{
+    return a.bf16 ? reverse_t<__nv_bfloat16>(a, w, d_o, dS_final, dv, dS0) : reverse_t<float>(a, w, d_o, dS_final, dv, dS0);
+}
+
+cudaError_t launch_grad(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg, float *dbeta)
+{
+    return a.bf16 ? grad_t<__nv_bfloat16>(a, w, d_o, dq, dk, dg, dbeta) : grad_t<float>(a, w, d_o, dq, dk, dg, dbeta);
+}
+
+cudaError_t launch_state_copy(const float *S0, float *S_final, size_t n, cudaStream_t stream)
+{
+    const unsigned grid = (unsigned)std::min<size_t>((n + 255) / 256, 148 * 8);
+    return launch_kernel(state_copy_kernel, dim3(grid), dim3(256), 0, stream, 1, S0, S_final, n);
+}
+
+}  // namespace gdelta
+}  // namespace mlstm

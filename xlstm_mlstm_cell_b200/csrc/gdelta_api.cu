@@ -37,6 +37,10 @@ size_t plan(char *base, const Args &a, bool backward, Workspace *w)
     };
     w->status = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t)));
     w->A = reinterpret_cast<float2 *>(take(sizeof(float2) * 64 * chunks));
+    if (!backward && tc_supported(a.bf16, a.DK, a.DV)) {
+        w->TG = reinterpret_cast<uint8_t *>(take(32768 * chunks));
+        return off;
+    }
     w->T = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
     w->P = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
     if (backward) {
@@ -94,7 +98,8 @@ size_t gdelta_bwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, 
 
 int gdelta_fwd_tensor_path(int DK, int DV, mlstm_dtype dt)
 {
-    return check_shape(dt, 1, 1, 1, 1, DK, DV) == MLSTM_OK ? 0 : -1;
+    if (check_shape(dt, 1, 1, 1, 1, DK, DV) != MLSTM_OK) return -1;
+    return tc_supported(dt == MLSTM_BF16, DK, DV) ? 1 : 0;
 }
 
 mlstm_status gdelta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,
@@ -119,6 +124,7 @@ mlstm_status gdelta_fwd(const void *q, const void *k, const void *v, const float
             e = launch_state_copy(S0, S_final, (size_t)B * NHV * DK * DV, a.stream);
         return cuda_status(e);
     }
+    if (w.TG) return cuda_status(launch_fwd_tc(a, w, o, S_final));
     cudaError_t e = launch_prep(a, w, false);
     if (e == cudaSuccess) e = launch_walk(a, w, o, S_final, false);
     return cuda_status(e);

@@ -45,6 +45,9 @@ cudaError_t launch_reverse(const Args &a, const Workspace &w, const void *d_o, c
 // dq, dk, dg, dbeta of every chunk from the workspace.
 cudaError_t launch_grad(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
                         float *dbeta);
+// The forward pass on the tensor cores (workspace: A, TG), and the shapes it takes.
+bool tc_supported(bool bf16, int DK, int DV);
+cudaError_t launch_fwd_tc(const Args &a, const Workspace &w, void *o, float *S_final);
 cudaError_t launch_state_copy(const float *S0, float *S_final, size_t n, cudaStream_t stream);
 
 struct StepArgs {

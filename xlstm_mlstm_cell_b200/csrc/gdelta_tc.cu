@@ -1,0 +1,588 @@
+// gdelta_tc.cu -- the gated delta rule's forward pass on the 5th-generation tensor cores (tcgen05), for
+// bf16 inputs with 64 <= DK <= 128.
+//
+// With S the state at a chunk's start (64 tokens) and a its cumulative log gates:
+//   prep  KK = strict_lower(D * K K^T), P = lower(D * Q K^T), T = (I + KK diag(beta))^-1, G = P diag(beta) T
+//   walk  X = [K; Q] S;  Y = V - e^a X_K;  [E - Y; F] = [T - I; G] Y;  O = scale (e^a X_Q + F);
+//         S' = e^{a_64} S + K^T (e^{a_64 - a} beta E)
+// G puts the scores' product with the chunk's corrections into the same MMA as T's, so a chunk is a chain
+// of three MMA groups, each followed by one pass of the epilogue warps over its accumulator.  Only that
+// chain is sequential; a CTA runs it for one value head and VT of its value columns.
+//
+// Operands.  K and Q are stacked in shared memory, 64 rows each, so that one M = 128 MMA serves both;
+// the same K tile, read MN-major, is the A operand of the state's update.  The fp32 operands S, Y, N =
+// e^{a_64 - a} beta E enter as three bf16 parts each, value, rounding residue and the residue's residue,
+// which hold all 24 bits, side by side along N: one MMA reads A once for all three, and the epilogue adds
+// the parts' columns.  T - I and G enter as two parts (rms error 2.7e-6 of the correction they carry); K, Q
+// are exact.  Without its unit diagonal T leaves Y itself out of the MMA: the threads that formed Y in fp32
+// add it to the result.  The fp32 state itself stays in the epilogue
+// threads' registers, a row (key element) of 16 columns each, and takes the update with fp32 additions.
+//
+// Roles: warp 0 one TMA thread, warp 1 the MMA thread (and the TMEM allocation), then 4 epilogue warps per
+// 16 value columns.  TMEM lane = token (K rows in lanes 0..63, Q rows in 64..127) or key element, so gates
+// and values are per lane, and no epilogue step exchanges anything between threads.  Every wait is bounded.
+#include "gdelta_prep.cuh"
+#include "tc_common.cuh"
+#include "tc_fwd.h"
+
+namespace mlstm {
+namespace gdelta {
+namespace {
+
+using namespace tc;
+
+// One contiguous copy global -> shared (16-byte aligned, a multiple of 16 bytes), completing on `bar`.
+MLSTM_DEVINL void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// 16 consecutive values of a row as three bf16 parts (the value, its rounding residue and that one's:
+// together the 24 bits of fp32) into a swizzled tile of `rows` rows: 16-byte chunks j0, j0 + 1 of the
+// row, the second and third parts `step` and 2 `step` chunks further.
+MLSTM_DEVINL void store_parts(uint8_t *tile, uint32_t row, uint32_t j0, uint32_t step, uint32_t rows, const float (&x)[16])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t h[4], m[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float x0 = x[c * 8 + 2 * e], x1 = x[c * 8 + 2 * e + 1];
+            h[e] = pack_bf16(x0, x1);
+            x0 -= __uint_as_float(h[e] << 16);
+            x1 -= __uint_as_float(h[e] & 0xffff0000u);
+            m[e] = pack_bf16(x0, x1);
+            l[e] = pack_bf16(x0 - __uint_as_float(m[e] << 16), x1 - __uint_as_float(m[e] & 0xffff0000u));
+        }
+        *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + c, rows)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + step + c, rows)) = make_uint4(m[0], m[1], m[2], m[3]);
+        *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + 2 * step + c, rows)) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+// 16 columns of an accumulator whose operand came in three parts, `step` columns apart: their sum.
+MLSTM_DEVINL void load_parts(uint32_t taddr, uint32_t step, float (&x)[16])
+{
+    uint32_t h[16], m[16], l[16];
+    tmem_ld16(taddr, h);
+    tmem_ld16(taddr + step, m);
+    tmem_ld16(taddr + 2 * step, l);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        x[i] = __uint_as_float(h[i]) + (__uint_as_float(m[i]) + __uint_as_float(l[i]));
+}
+
+// ---------------------------------------------------------------- prep
+
+namespace prep {
+constexpr int THREADS = 128;
+constexpr uint32_t KQ = 0;                              // [2 blocks][128 rows][64] K over Q, until its product is done; then
+constexpr uint32_t MR = 0;                              // [64][LDT] floats: I + KK diag(beta), then T, row-major
+constexpr uint32_t MC = MR + 64 * LDT * 4;              // [64][LDT] its transpose
+constexpr uint32_t PC = MC + 64 * LDT * 4;              // [64][LDT] transpose of P diag(beta)
+constexpr uint32_t BT = PC + 64 * LDT * 4;              // [64] beta
+constexpr uint32_t AC = BT + 256;                       // [64] float2
+constexpr uint32_t BAR = AC + 512;
+constexpr uint32_t TOTAL = BAR + 32 + 1024;
+static_assert(PC >= 32768, "the K, Q tile lies below P");
+
+// D[r][c] (+)= sign sum_l A[r][l] B[l][c] on 4 x 4 tiles, A given transposed (ac[l][r]), B by rows.
+MLSTM_DEVINL void tile4(const float *ac, const float *br, int r, int c, int l0, int l1, float (&acc)[4][4])
+{
+    for (int l = l0; l < l1; ++l) {
+        const float4 x = *reinterpret_cast<const float4 *>(ac + l * LDT + r);
+        const float4 y = *reinterpret_cast<const float4 *>(br + l * LDT + c);
+        const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv[i], yv[j], acc[i][j]);
+    }
+}
+
+// Joins the inverses of two diagonal blocks of N at `at`: with C the block below the first,
+// the inverse has -D^-1 C A^-1 in its place.  `tid` of (N / 4)^2 threads, `sync` among them and the
+// other joins'.  The intermediate C A^-1 goes to the (zero) block above, which is cleared again.
+template <int N, typename Sync>
+MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync)
+{
+    const int r = (tid / (N / 4)) * 4, c = (tid % (N / 4)) * 4;
+    float acc[4][4] = {};
+    if (on) tile4(mc + at * LDT + at + N, mr + at * LDT + at, r, c, c, N, acc);   // C A^-1, A^-1 lower
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4 *>(mr + (at + r + i) * LDT + at + N + c) =
+                make_float4(-acc[i][0], -acc[i][1], -acc[i][2], -acc[i][3]);
+    }
+    sync();
+    float out[4][4] = {};
+    if (on) tile4(mc + (at + N) * LDT + at + N, mr + at * LDT + at + N, r, c, 0, r + 4, out);   // D^-1 lower
+    sync();
+    if (on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<float4 *>(mr + (at + N + r + i) * LDT + at + c) =
+                make_float4(out[i][0], out[i][1], out[i][2], out[i][3]);
+            *reinterpret_cast<float4 *>(mc + (at + c + i) * LDT + at + N + r) =
+                make_float4(out[0][i], out[1][i], out[2][i], out[3][i]);
+            *reinterpret_cast<float4 *>(mr + (at + r + i) * LDT + at + N + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    sync();
+}
+}  // namespace prep
+
+// One CTA per chunk and key head: [K; Q] K^T once in TMEM, then the matrices of every value head on it.
+// The inverse (see invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
+// tiles fed by two 16-byte loads per reduction step; four CTAs an SM overlap their short serial parts.
+__global__ void __launch_bounds__(prep::THREADS, 4)
+prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const float *__restrict__ g, const float *__restrict__ beta, const int *__restrict__ lengths, int NH,
+               int NHV, int S, int DK, Workspace w)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float *mr = reinterpret_cast<float *>(smem + prep::MR), *mc = reinterpret_cast<float *>(smem + prep::MC);
+    float *pc = reinterpret_cast<float *>(smem + prep::PC), *bt = reinterpret_cast<float *>(smem + prep::BT);
+    float2 *a = reinterpret_cast<float2 *>(smem + prep::AC);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + prep::BAR);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2), *abort_flag = tmem_slot + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
+    WaitCtx wc{abort_flag, w.status};
+    if (tid == 0) {
+        mbar_init(&bars[0], 1);
+        mbar_init(&bars[1], 1);
+        *abort_flag = 0u;
+        fence_barrier_init();
+        tma_prefetch(&tm_q);
+        tma_prefetch(&tm_k);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 64);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+    if (c == 0 && bh == 0 && tid == 0) *w.status = 0u;
+    const int len = min(CH, live_tokens(lengths, b, S) - c * CH);
+    if (len > 0) {
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&bars[0], 32768);
+            for (int kb = 0; kb < 2; ++kb) {
+                tma_load_3d(smem + kb * 16384, &tm_k, 64 * kb, c * CH, bh, &bars[0]);
+                tma_load_3d(smem + kb * 16384 + 8192, &tm_q, 64 * kb, c * CH, bh, &bars[0]);
+            }
+            if (mbar_wait(&bars[0], 0, wc)) {
+                constexpr uint32_t ID = idesc_bf16(128, 64, 0, 0);
+                const uint64_t d = smem_desc(smem_u32(smem), 16, 1024);
+                for (int kk = 0; kk * 16 < DK; ++kk) {   // behind DK both operands are zero
+                    const uint64_t dk = d + (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+                    mma_ss(tmem, dk, dk, ID, kk > 0);
+                }
+                mma_commit(&bars[1]);
+            }
+        }
+        __syncwarp();
+        bool ok = true;
+        const int i = tid & 63;   // the thread's row: of K K^T in warps 0 and 1, of Q K^T in 2 and 3
+        const bool krow = tid < 64;
+        for (int h = 0; h < group; ++h) {
+            const int bhv = b * NHV + (bh % NH) * group + h;
+            const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
+            if (warp == 0) chunk_gates(g + gt, len, lane, a);
+            else if (tid >= 64) bt[i] = i < len ? beta[gt + i] : 0.f;
+            __syncthreads();
+            if (h == 0) {
+                ok = mbar_wait(&bars[1], 0, wc);
+                tc_fence_after();
+            }
+            if (krow) w.A[ch * 64 + i] = a[i];
+            const float2 ai = a[i];
+            // rows and columns behind `len` hold whatever the padding does: selected away
+            const int top = i < len ? (krow ? i : i + 1) : 0;
+#pragma unroll
+            for (int half = 0; half < 4; ++half) {   // 16 columns
+                float x[16];
+                {
+                    uint32_t r[16];
+                    tmem_ld16(tmem_addr(tmem, warp * 32, half * 16), r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) x[s] = __uint_as_float(r[s]);
+                }
+                // whole blocks above the diagonal need no exponentials
+                if (16 * half <= 32 * (warp & 1) + 31) {
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) {
+                        const int j = half * 16 + s;
+                        x[s] = j < top ? expf(gate_diff(ai, a[j])) * x[s] * bt[j] : 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) x[s] = 0.f;
+                }
+                if (krow) {
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) mc[(half * 16 + s) * LDT + i] = x[s];
+#pragma unroll
+                    for (int s = 0; s < 16; s += 4)
+                        *reinterpret_cast<float4 *>(mr + i * LDT + half * 16 + s) = make_float4(x[s], x[s + 1], x[s + 2], x[s + 3]);
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 16; ++s) pc[(half * 16 + s) * LDT + i] = x[s];
+                }
+            }
+            __syncthreads();
+            if (krow) {   // diagonal blocks of 16: thread (block, column j) solves (I + M_b) x = e_j
+                const int at = tid & 48, j = tid & 15;
+                float x[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    float s = r == j ? 1.f : 0.f;
+#pragma unroll
+                    for (int l = 0; l < r; ++l) s = fmaf(-mr[(at + r) * LDT + at + l], x[l], s);
+                    x[r] = s;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mr[(at + r) * LDT + at + j] = x[r];
+#pragma unroll
+                for (int r = 0; r < 16; r += 4)
+                    *reinterpret_cast<float4 *>(mc + (at + j) * LDT + at + r) = make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+            }
+            __syncthreads();
+            prep::join<16>(mr, mc, (tid >> 4 & 1) * 32, tid & 15, tid < 32, [] { __syncthreads(); });
+            prep::join<32>(mr, mc, 0, tid & 63, tid < 64, [] { __syncthreads(); });
+            // G = P diag(beta) T and [T - I; G] as two bf16 parts, each a swizzled tile of 128 rows of 64
+            uint8_t *tg = w.TG + ch * 32768;
+#pragma unroll
+            for (int rep = 0; rep < 2; ++rep) {
+                const int i0 = rep * 32 + (tid >> 4) * 4, c0 = (tid & 15) * 4;
+                float acc[4][4] = {};
+                prep::tile4(pc, mr, i0, c0, c0, i0 + 4, acc);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float4 t4 = *reinterpret_cast<const float4 *>(mr + (i0 + r) * LDT + c0);
+                    const float t[4] = {t4.x, t4.y, t4.z, t4.w};
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = part ? acc[r][e] : i0 + r == c0 + e ? 0.f : t[e];
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            hi[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                            lo[e] = pack_bf16(y[2 * e] - __uint_as_float(hi[e] << 16),
+                                              y[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                        }
+                        const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
+                        *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
+                        *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (!ok && tid == 0) mbar_wait_drain(&bars[0], 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 64);
+    }
+}
+
+// ---------------------------------------------------------------- walk
+
+template <int VT>
+struct Walk {
+    static constexpr int NCG = VT / 16;                    // column groups of 16
+    static constexpr int EPI = 4 * NCG;                    // epilogue warps
+    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int STAGES = 2;
+    static constexpr uint32_t STAGE = 65536;               // [K; Q] 32 KB, [T; G] values and residues 16 KB each
+    static constexpr uint32_t SP = STAGES * STAGE;         // S parts: 128 rows, 3 VT columns (in blocks of 64)
+    static constexpr uint32_t BLOCKS = (3 * VT + 63) / 64;
+    static constexpr uint32_t YN = SP + BLOCKS * 16384;    // Y parts, then N parts: 64 rows
+    static constexpr uint32_t BAR = YN + BLOCKS * 8192;
+    static constexpr uint32_t NBAR = 2 * STAGES + 6;
+    static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
+    static constexpr uint32_t TMEM_COLS = VT == 64 ? 512 : 256;   // X and then D, [E; F]: 3 VT each
+};
+
+struct WalkParams {
+    const __nv_bfloat16 *v;
+    const float *beta, *S0;
+    const int *lengths;
+    __nv_bfloat16 *o;
+    float *S_final;
+    int NH, NHV, S, DK, DV;
+    float scale;
+    Workspace w;
+};
+
+template <int VT, int KS>
+__global__ void __launch_bounds__(Walk<VT>::THREADS, 1)
+walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WalkParams p)
+{
+    using W = Walk<VT>;
+    constexpr int NST = W::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + W::BAR);
+    uint64_t *full = bars, *empty = bars + NST, *s_ready = bars + 2 * NST, *x_done = s_ready + 1, *y_ready = s_ready + 2,
+             *e_done = s_ready + 3, *n_ready = s_ready + 4, *d_done = s_ready + 5;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + W::NBAR), *abort_flag = tmem_slot + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int bhv = blockIdx.y, b = bhv / p.NHV, bh = b * p.NH + (bhv % p.NHV) / (p.NHV / p.NH);
+    WaitCtx wc{abort_flag, p.w.status};
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(s_ready, W::EPI);
+        mbar_init(x_done, 1);
+        mbar_init(y_ready, W::EPI / 2);
+        mbar_init(e_done, 1);
+        mbar_init(n_ready, W::EPI);
+        mbar_init(d_done, 1);
+        *abort_flag = 0u;
+        fence_barrier_init();
+        tma_prefetch(&tm_q);
+        tma_prefetch(&tm_k);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, W::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int n = live_tokens(p.lengths, b, p.S), nc = (n + CH - 1) / CH;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % NST;
+                if (c >= NST && !mbar_wait(&empty[st], (uint32_t)(c / NST - 1) & 1u, wc)) break;
+                uint8_t *s = smem + st * W::STAGE;
+                mbar_arrive_expect_tx(&full[st], W::STAGE);
+                for (int kb = 0; kb < 2; ++kb) {
+                    tma_load_3d(s + kb * 16384, &tm_k, 64 * kb, c * CH, bh, &full[st]);
+                    tma_load_3d(s + kb * 16384 + 8192, &tm_q, 64 * kb, c * CH, bh, &full[st]);
+                }
+                bulk_load(s + 32768, p.w.TG + ((size_t)bhv * p.w.NC + c) * 32768, 32768, &full[st]);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // A K-major (X, E) or MN-major (D), B MN-major; N = the parts' columns side by side, so that A is
+            // read once for all of them
+            constexpr uint32_t IDX = idesc_bf16(128, 3 * VT, 0, 1), IDM = idesc_bf16(128, 2 * VT, 0, 1);
+            constexpr uint32_t IDD = idesc_bf16(128, 3 * VT, 1, 1);
+            const uint64_t bs = smem_desc(smem_u32(smem + W::SP), 16384, 1024);
+            const uint64_t by = smem_desc(smem_u32(smem + W::YN), 8192, 1024);
+            const uint64_t ak = smem_desc(smem_u32(smem), 16, 1024), at = smem_desc(smem_u32(smem) + 32768, 16, 1024);
+            const uint64_t ad = smem_desc(smem_u32(smem), 16384, 1024);
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % NST;
+                const uint64_t so = (uint64_t)st * (W::STAGE / 16);
+                const uint32_t ph = (uint32_t)c & 1u;
+                if (!mbar_wait(&full[st], (uint32_t)(c / NST) & 1u, wc)) break;
+                if (!mbar_wait(s_ready, ph, wc)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    mma_ss(tmem, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), bs + (uint64_t)(k * 128), IDX, k > 0);
+                mma_commit(x_done);
+                if (!mbar_wait(y_ready, ph, wc)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_ss(tmem + 3 * VT, at + so + (uint64_t)(k * 2), by + (uint64_t)(k * 128), IDX, k > 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
+                    mma_ss(tmem + 3 * VT, at + so + (uint64_t)(1024 + k * 2), by + (uint64_t)(k * 128), IDM, 1);
+                mma_commit(e_done);
+                if (!mbar_wait(n_ready, ph, wc)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // over X, which every warp has read
+                    mma_ss(tmem, ad + so + (uint64_t)(k * 128), by + (uint64_t)(k * 128), IDD, k > 0);
+                mma_commit(d_done);
+                mma_commit(&empty[st]);
+            }
+        }
+    } else {
+        const int quad = warp & 3, cg = (warp - 2) >> 2;
+        const int row = quad * 32 + lane, t = row & 63;        // TMEM lane; token of the chunk
+        const bool krow = quad < 2;
+        const int col = blockIdx.x * VT + cg * 16;             // first of the thread's 16 value columns
+        const uint32_t tl = tmem_addr(tmem, quad * 32, cg * 16);
+        uint8_t *sp = smem + W::SP, *yn = smem + W::YN;
+        float s[16];                                           // row `row` of the state
+        const size_t srow = ((size_t)bhv * p.DK + row) * p.DV + col;
+        const int live_cols = min(16, p.DV - col);             // a multiple of 8, may be <= 0
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const float4 x = p.S0 && row < p.DK && e < live_cols ? *reinterpret_cast<const float4 *>(p.S0 + srow + e)
+                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            s[e] = x.x; s[e + 1] = x.y; s[e + 2] = x.z; s[e + 3] = x.w;
+        }
+        uint4 vr[2];
+        float2 at = {}, al = {};
+        float btv = 0.f;
+        auto prefetch = [&](int c) {   // the token's value row, gates and write strength
+            const int tok = c * CH + t;
+            const float2 *A = p.w.A + ((size_t)bhv * p.w.NC + c) * 64;
+            at = A[t];
+            al = A[63];
+            btv = tok < n ? p.beta[(size_t)bhv * p.S + tok] : 0.f;
+            const __nv_bfloat16 *v = p.v + ((size_t)bhv * p.S + tok) * p.DV + col;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                vr[e] = krow && tok < n && 8 * e < live_cols ? *reinterpret_cast<const uint4 *>(v + 8 * e)
+                                                             : make_uint4(0u, 0u, 0u, 0u);
+        };
+        if (nc > 0) prefetch(0);
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = (uint32_t)c & 1u;
+            const int len = min(CH, n - c * CH);
+            store_parts(sp, row, cg * 2, VT / 8, 128, s);
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_ready);
+            const float ea = expf(at.x + at.y), eo = expf(gate_diff(al, at)) * btv, ef = expf(al.x + al.y);
+            float x[16];
+            if (!mbar_wait(x_done, ph, wc)) break;
+            tc_fence_after();
+            load_parts(tl, VT, x);
+            if (krow) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 v2 = unpack_bf16((&vr[e >> 2].x)[e & 3]);
+                    x[2 * e] = t < len ? fmaf(-ea, x[2 * e], v2.x) : 0.f;
+                    x[2 * e + 1] = t < len ? fmaf(-ea, x[2 * e + 1], v2.y) : 0.f;
+                }
+                store_parts(yn, row, cg * 2, VT / 8, 64, x);
+                fence_proxy_async();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(y_ready);
+            } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(n_ready);   // X is read
+            }
+            if (c + 1 < nc) prefetch(c + 1);
+            float y[16];
+            if (!mbar_wait(e_done, ph, wc)) break;
+            tc_fence_after();
+            load_parts(tl + 3 * VT, VT, y);
+            if (krow) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = eo * (x[e] + y[e]);
+                store_parts(yn, row, cg * 2, VT / 8, 64, y);
+                if (cg == 0 && t >= len) {   // padding: its keys meet N's zeros, which NaN would survive
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<uint4 *>(smem + (c % NST) * W::STAGE + sw128_chunk(t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(n_ready);
+            } else if (t < len) {
+                __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + c * CH + t) * p.DV + col;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (8 * e >= live_cols) break;
+                    uint32_t z[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        z[u] = pack_bf16(p.scale * fmaf(ea, x[8 * e + 2 * u], y[8 * e + 2 * u]),
+                                         p.scale * fmaf(ea, x[8 * e + 2 * u + 1], y[8 * e + 2 * u + 1]));
+                    *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(z[0], z[1], z[2], z[3]);
+                }
+            }
+            if (!mbar_wait(d_done, ph, wc)) break;
+            tc_fence_after();
+            load_parts(tl, VT, y);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[e] = fmaf(ef, s[e], y[e]);
+        }
+        if (p.S_final && row < p.DK) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                if (e < live_cols) *reinterpret_cast<float4 *>(p.S_final + srow + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+        }
+        for (int r = n + (int)threadIdx.x - 64; r < p.S; r += 32 * W::EPI) {   // padding rows
+            __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + r) * p.DV + blockIdx.x * VT;
+            for (int e = 0; e < VT && (int)blockIdx.x * VT + e < p.DV; e += 8)
+                *reinterpret_cast<uint4 *>(o + e) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*reinterpret_cast<volatile uint32_t *>(abort_flag)) {
+        // a wait gave up: let MMAs and copies this CTA may still have in flight finish (bounded)
+        const unsigned long long tb = global_timer();
+        while (global_timer() - tb < 100000ull) { }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, W::TMEM_COLS);
+    }
+}
+
+template <int VT, int KS>
+cudaError_t launch_walk_vt(const Args &a, const Workspace &w, const CUtensorMap &mq, const CUtensorMap &mk, void *o,
+                           float *S_final)
+{
+    cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<VT, KS>, Walk<VT>::TOTAL);
+    if (e != cudaSuccess) return e;
+    WalkParams p = {static_cast<const __nv_bfloat16 *>(a.v), a.beta, a.S0, a.lengths, static_cast<__nv_bfloat16 *>(o),
+                    S_final, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w};
+    return launch_kernel(walk_tc_kernel<VT, KS>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(Walk<VT>::THREADS),
+                         Walk<VT>::TOTAL, a.stream, 1, mq, mk, p);
+}
+
+}  // namespace
+
+bool tc_supported(bool bf16, int DK, int DV) { return bf16 && DK >= 64 && DV >= 32; }
+
+cudaError_t launch_fwd_tc(const Args &a, const Workspace &w, void *o, float *S_final)
+{
+    CUtensorMap mq, mk;
+    if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
+        return cudaErrorUnknown;
+    cudaError_t e = ensure_dynamic_smem((const void *)prep_tc_kernel, prep::TOTAL);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(prep_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, mq, mk, a.g,
+                      a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, w);
+    if (e != cudaSuccess) return e;
+    // a chunk takes longer the more columns a CTA has, so the columns are split while the GPU has SMs for it
+    const bool narrow = (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
+    if (a.DK > 64)
+        return narrow ? launch_walk_vt<32, 8>(a, w, mq, mk, o, S_final) : launch_walk_vt<64, 8>(a, w, mq, mk, o, S_final);
+    return narrow ? launch_walk_vt<32, 4>(a, w, mq, mk, o, S_final) : launch_walk_vt<64, 4>(a, w, mq, mk, o, S_final);
+}
+
+}  // namespace gdelta
+}  // namespace mlstm

@@ -23,21 +23,31 @@ MLSTM_DEVINL float gate_diff(float2 x, float2 y) { return (x.x - y.x) + (x.y - y
 MLSTM_DEVINL float clamp_gate(float g) { return g < -128.f ? -128.f : g; }
 
 // One warp: the cumulative log gates of a chunk's 64 tokens (`len` of them live, the others 0), summed
-// in fp64 and kept as value and residue.
-MLSTM_DEVINL void chunk_gates(const float *g, int len, int lane, float2 *a)
+// in fp64, times `unit`, and kept as value and residue: tokens 2 lane (a0) and 2 lane + 1 (a1).
+MLSTM_DEVINL void chunk_gates(const float *g, int len, int lane, double unit, float2 &a0, float2 &a1)
 {
-    double x0 = 2 * lane < len ? (double)clamp_gate(g[2 * lane]) : 0.0;
-    double x1 = 2 * lane + 1 < len ? (double)clamp_gate(g[2 * lane + 1]) : 0.0;
+    const double x0 = 2 * lane < len ? (double)clamp_gate(g[2 * lane]) : 0.0;
+    const double x1 = 2 * lane + 1 < len ? (double)clamp_gate(g[2 * lane + 1]) : 0.0;
     double sum = x0 + x1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const double y = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += y;
     }
-    const double c0 = sum - x1;
-    const float h0 = (float)c0, h1 = (float)sum;
-    a[2 * lane] = make_float2(h0, (float)(c0 - (double)h0));
-    a[2 * lane + 1] = make_float2(h1, (float)(sum - (double)h1));
+    const double c0 = (sum - x1) * unit, c1 = sum * unit;
+    a0.x = (float)c0;
+    a0.y = (float)(c0 - (double)a0.x);
+    a1.x = (float)c1;
+    a1.y = (float)(c1 - (double)a1.x);
+}
+MLSTM_DEVINL void chunk_gates(const float *g, int len, int lane, float2 *a)
+{
+    chunk_gates(g, len, lane, 1.0, a[2 * lane], a[2 * lane + 1]);
+}
+// The same in units of log 2, for exp2f.
+MLSTM_DEVINL void chunk_gates_log2(const float *g, int len, int lane, float2 &a0, float2 &a1)
+{
+    chunk_gates(g, len, lane, 1.4426950408889634074, a0, a1);
 }
 
 constexpr int LDT = 68;   // row stride of the 64 x 64 matrices in shared memory (16-byte rows, no bank repeats)

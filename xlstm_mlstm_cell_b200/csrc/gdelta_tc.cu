@@ -39,31 +39,37 @@ MLSTM_DEVINL void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t
                  : "memory");
 }
 
-// 16 consecutive values of a row as three bf16 parts (the value, its rounding residue and that one's:
-// together the 24 bits of fp32) into a swizzled tile of `rows` rows: 16-byte chunks j0, j0 + 1 of the
-// row, the second and third parts `step` and 2 `step` chunks further.
-MLSTM_DEVINL void store_parts(uint8_t *tile, uint32_t row, uint32_t j0, uint32_t step, uint32_t rows, const float (&x)[16])
+// Eight pairs of values of a row as three bf16 parts, whose sum is exactly the fp32 value: the top 8
+// significant bits, the next 8 and the last 8 (cut off, not rounded, so packing is a byte permutation),
+// into a swizzled tile of `rows` rows: 16-byte chunks j0, j0 + 1 of the row, the second and third parts
+// `step` and 2 `step` chunks further.
+MLSTM_DEVINL void store_parts(uint8_t *tile, uint32_t row, uint32_t j0, uint32_t step, uint32_t rows,
+                              const uint64_t (&x)[8])
 {
+    const uint64_t neg = f2_pack(-1.f, -1.f);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        uint32_t h[4], m[4], l[4];
+        uint32_t part[3][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float x0 = x[c * 8 + 2 * e], x1 = x[c * 8 + 2 * e + 1];
-            h[e] = pack_bf16(x0, x1);
-            x0 -= __uint_as_float(h[e] << 16);
-            x1 -= __uint_as_float(h[e] & 0xffff0000u);
-            m[e] = pack_bf16(x0, x1);
-            l[e] = pack_bf16(x0 - __uint_as_float(m[e] << 16), x1 - __uint_as_float(m[e] & 0xffff0000u));
+            uint64_t r = x[c * 4 + e];
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                const float2 v = f2_unpack(r);
+                const uint32_t u0 = __float_as_uint(v.x), u1 = __float_as_uint(v.y);
+                part[q][e] = __byte_perm(u0, u1, 0x7632);
+                if (q < 2) r = f2_fma(f2_pack(__uint_as_float(u0 & 0xffff0000u), __uint_as_float(u1 & 0xffff0000u)), neg, r);
+            }
         }
-        *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + c, rows)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + step + c, rows)) = make_uint4(m[0], m[1], m[2], m[3]);
-        *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + 2 * step + c, rows)) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+            *reinterpret_cast<uint4 *>(tile + sw128_chunk(row, j0 + q * step + c, rows)) =
+                make_uint4(part[q][0], part[q][1], part[q][2], part[q][3]);
     }
 }
 
 // 16 columns of an accumulator whose operand came in three parts, `step` columns apart: their sum.
-MLSTM_DEVINL void load_parts(uint32_t taddr, uint32_t step, float (&x)[16])
+MLSTM_DEVINL void load_parts(uint32_t taddr, uint32_t step, uint64_t (&x)[8])
 {
     uint32_t h[16], m[16], l[16];
     tmem_ld16(taddr, h);
@@ -71,8 +77,10 @@ MLSTM_DEVINL void load_parts(uint32_t taddr, uint32_t step, float (&x)[16])
     tmem_ld16(taddr + 2 * step, l);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        x[i] = __uint_as_float(h[i]) + (__uint_as_float(m[i]) + __uint_as_float(l[i]));
+    for (int i = 0; i < 8; ++i) {
+        auto two = [&](const uint32_t (&r)[16]) { return f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])); };
+        x[i] = f2_add(two(h), f2_add(two(m), two(l)));
+    }
 }
 
 // ---------------------------------------------------------------- prep
@@ -83,52 +91,68 @@ constexpr uint32_t KQ = 0;                              // [2 blocks][128 rows][
 constexpr uint32_t MR = 0;                              // [64][LDT] floats: I + KK diag(beta), then T, row-major
 constexpr uint32_t MC = MR + 64 * LDT * 4;              // [64][LDT] its transpose
 constexpr uint32_t PC = MC + 64 * LDT * 4;              // [64][LDT] transpose of P diag(beta)
-constexpr uint32_t BT = PC + 64 * LDT * 4;              // [64] beta
-constexpr uint32_t AC = BT + 256;                       // [64] float2
-constexpr uint32_t BAR = AC + 512;
+constexpr uint32_t AC = PC + 64 * LDT * 4;              // [64] float4: cumulative log2 gate as value and residue, beta
+constexpr uint32_t BAR = AC + 1024;
 constexpr uint32_t TOTAL = BAR + 32 + 1024;
 static_assert(PC >= 32768, "the K, Q tile lies below P");
 
-// D[r][c] (+)= sign sum_l A[r][l] B[l][c] on 4 x 4 tiles, A given transposed (ac[l][r]), B by rows.
-MLSTM_DEVINL void tile4(const float *ac, const float *br, int r, int c, int l0, int l1, float (&acc)[4][4])
+// acc = sum_{l0 <= l < l1} A[r + 2 i .. ][l] B[l][c + j] on a tile of 2 RP rows x 4 columns, rows in pairs;
+// A given transposed (ac[l][r]), B by rows.
+template <int RP>
+MLSTM_DEVINL void tile(const float *ac, const float *br, int r, int c, int l0, int l1, uint64_t (&acc)[RP][4])
 {
+#pragma unroll
+    for (int i = 0; i < RP; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+#pragma unroll 4
     for (int l = l0; l < l1; ++l) {
-        const float4 x = *reinterpret_cast<const float4 *>(ac + l * LDT + r);
-        const float4 y = *reinterpret_cast<const float4 *>(br + l * LDT + c);
-        const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
+        uint64_t x[RP];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RP / 2; ++i) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(ac + l * LDT + r + 4 * i);
+            x[2 * i] = v.x;
+            x[2 * i + 1] = v.y;
+        }
+        const float4 y4 = *reinterpret_cast<const float4 *>(br + l * LDT + c);
+        const uint64_t y[4] = {f2_pack(y4.x, y4.x), f2_pack(y4.y, y4.y), f2_pack(y4.z, y4.z), f2_pack(y4.w, y4.w)};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv[i], yv[j], acc[i][j]);
+        for (int i = 0; i < RP; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = f2_fma(x[i], y[j], acc[i][j]);
     }
 }
 
 // Joins the inverses of two diagonal blocks of N at `at`: with C the block below the first,
-// the inverse has -D^-1 C A^-1 in its place.  `tid` of (N / 4)^2 threads, `sync` among them and the
-// other joins'.  The intermediate C A^-1 goes to the (zero) block above, which is cleared again.
+// the inverse has -D^-1 C A^-1 in its place.  Thread `tid` of (N / 4)^2, `sync` among all.  The intermediate
+// C A^-1 goes to the (zero) block above, which is cleared again.
 template <int N, typename Sync>
 MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync)
 {
     const int r = (tid / (N / 4)) * 4, c = (tid % (N / 4)) * 4;
-    float acc[4][4] = {};
-    if (on) tile4(mc + at * LDT + at + N, mr + at * LDT + at, r, c, c, N, acc);   // C A^-1, A^-1 lower
+    uint64_t acc[2][4];
     if (on) {
+        tile<2>(mc + at * LDT + at + N, mr + at * LDT + at, r, c, 0, N, acc);   // C A^-1
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4 *>(mr + (at + r + i) * LDT + at + N + c) =
-                make_float4(-acc[i][0], -acc[i][1], -acc[i][2], -acc[i][3]);
+        for (int i = 0; i < 4; ++i) {
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = i & 1 ? -f2_unpack(acc[i >> 1][j]).y : -f2_unpack(acc[i >> 1][j]).x;
+            *reinterpret_cast<float4 *>(mr + (at + r + i) * LDT + at + N + c) = make_float4(x[0], x[1], x[2], x[3]);
+        }
     }
     sync();
-    float out[4][4] = {};
-    if (on) tile4(mc + (at + N) * LDT + at + N, mr + at * LDT + at + N, r, c, 0, r + 4, out);   // D^-1 lower
+    if (on) tile<2>(mc + (at + N) * LDT + at + N, mr + at * LDT + at + N, r, c, 0, r + 4, acc);   // D^-1 lower
     sync();
     if (on) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            *reinterpret_cast<float4 *>(mr + (at + N + r + i) * LDT + at + c) =
-                make_float4(out[i][0], out[i][1], out[i][2], out[i][3]);
-            *reinterpret_cast<float4 *>(mc + (at + c + i) * LDT + at + N + r) =
-                make_float4(out[0][i], out[1][i], out[2][i], out[3][i]);
+            float x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = i & 1 ? f2_unpack(acc[i >> 1][j]).y : f2_unpack(acc[i >> 1][j]).x;
+            *reinterpret_cast<float4 *>(mr + (at + N + r + i) * LDT + at + c) = make_float4(x[0], x[1], x[2], x[3]);
+            const float2 lo = f2_unpack(acc[0][i]), hi = f2_unpack(acc[1][i]);
+            *reinterpret_cast<float4 *>(mc + (at + c + i) * LDT + at + N + r) = make_float4(lo.x, lo.y, hi.x, hi.y);
             *reinterpret_cast<float4 *>(mr + (at + r + i) * LDT + at + N + c) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
@@ -137,7 +161,8 @@ MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync
 }  // namespace prep
 
 // One CTA per chunk and key head: [K; Q] K^T once in TMEM, then the matrices of every value head on it.
-// The inverse (see invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
+// The inverse (diagonal blocks of 16 by substitution,
+// then joins, as invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
 // tiles fed by two 16-byte loads per reduction step; four CTAs an SM overlap their short serial parts.
 __global__ void __launch_bounds__(prep::THREADS, 4)
 prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -147,8 +172,8 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     float *mr = reinterpret_cast<float *>(smem + prep::MR), *mc = reinterpret_cast<float *>(smem + prep::MC);
-    float *pc = reinterpret_cast<float *>(smem + prep::PC), *bt = reinterpret_cast<float *>(smem + prep::BT);
-    float2 *a = reinterpret_cast<float2 *>(smem + prep::AC);
+    float *pc = reinterpret_cast<float *>(smem + prep::PC);
+    float4 *ga = reinterpret_cast<float4 *>(smem + prep::AC);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + prep::BAR);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 2), *abort_flag = tmem_slot + 1;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -198,15 +223,22 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int h = 0; h < group; ++h) {
             const int bhv = b * NHV + (bh % NH) * group + h;
             const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
-            if (warp == 0) chunk_gates(g + gt, len, lane, a);
-            else if (tid >= 64) bt[i] = i < len ? beta[gt + i] : 0.f;
+            if (warp == 0) {
+                float2 a0, a1;
+                const float b0 = 2 * lane < len ? beta[gt + 2 * lane] : 0.f;
+                const float b1 = 2 * lane + 1 < len ? beta[gt + 2 * lane + 1] : 0.f;
+                chunk_gates_log2(g + gt, len, lane, a0, a1);
+                ga[2 * lane] = make_float4(a0.x, a0.y, b0, 0.f);
+                ga[2 * lane + 1] = make_float4(a1.x, a1.y, b1, 0.f);
+            }
             __syncthreads();
             if (h == 0) {
                 ok = mbar_wait(&bars[1], 0, wc);
                 tc_fence_after();
             }
-            if (krow) w.A[ch * 64 + i] = a[i];
-            const float2 ai = a[i];
+            const float4 ai = ga[i];
+            // what the walk needs of the gates: e^a of the token, and beta e^{a_64 - a}
+            if (krow) w.A[ch * 64 + i] = make_float2(exp2f(ai.x + ai.y), ai.z * exp2f((ga[63].x - ai.x) + (ga[63].y - ai.y)));
             // rows and columns behind `len` hold whatever the padding does: selected away
             const int top = i < len ? (krow ? i : i + 1) : 0;
 #pragma unroll
@@ -224,7 +256,10 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int s = 0; s < 16; ++s) {
                         const int j = half * 16 + s;
-                        x[s] = j < top ? expf(gate_diff(ai, a[j])) * x[s] * bt[j] : 0.f;
+                        const float4 aj = ga[j];
+                        const bool on = j < top;   // selects, not a branch a column
+                        const float d = on ? (ai.x - aj.x) + (ai.y - aj.y) : 0.f, y = on ? x[s] * aj.z : 0.f;
+                        x[s] = exp2f(d) * y;
                     }
                 } else {
 #pragma unroll
@@ -247,10 +282,16 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 float x[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
-                    float s = r == j ? 1.f : 0.f;
+                    float s0 = r == j ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int l = 0; l < r; ++l) s = fmaf(-mr[(at + r) * LDT + at + l], x[l], s);
-                    x[r] = s;
+                    for (int l = 0; l < r; l += 4) {   // M is zero from its diagonal on
+                        const float4 y = *reinterpret_cast<const float4 *>(mr + (at + r) * LDT + at + l);
+                        s0 = fmaf(-y.x, x[l], s0);
+                        if (l + 1 < r) s1 = fmaf(-y.y, x[l + 1], s1);
+                        if (l + 2 < r) s0 = fmaf(-y.z, x[l + 2], s0);
+                        if (l + 3 < r) s1 = fmaf(-y.w, x[l + 3], s1);
+                    }
+                    x[r] = s0 + s1;
                 }
                 __syncwarp();
 #pragma unroll
@@ -264,31 +305,31 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             prep::join<32>(mr, mc, 0, tid & 63, tid < 64, [] { __syncthreads(); });
             // G = P diag(beta) T and [T - I; G] as two bf16 parts, each a swizzled tile of 128 rows of 64
             uint8_t *tg = w.TG + ch * 32768;
+            const int i0 = (tid >> 4) * 8, c0 = (tid & 15) * 4;
+            uint64_t acc[4][4];
+            prep::tile<4>(pc, mr, i0, c0, 0, i0 + 8, acc);   // from 0: one address for all columns
 #pragma unroll
-            for (int rep = 0; rep < 2; ++rep) {
-                const int i0 = rep * 32 + (tid >> 4) * 4, c0 = (tid & 15) * 4;
-                float acc[4][4] = {};
-                prep::tile4(pc, mr, i0, c0, c0, i0 + 4, acc);
+            for (int r = 0; r < 8; ++r) {
+                const float4 t4 = *reinterpret_cast<const float4 *>(mr + (i0 + r) * LDT + c0);
+                const float t[4] = {t4.x, t4.y, t4.z, t4.w};
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float4 t4 = *reinterpret_cast<const float4 *>(mr + (i0 + r) * LDT + c0);
-                    const float t[4] = {t4.x, t4.y, t4.z, t4.w};
+                for (int part = 0; part < 2; ++part) {
+                    float y[4];
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        float y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = part ? acc[r][e] : i0 + r == c0 + e ? 0.f : t[e];
-                        uint32_t hi[2], lo[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            hi[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-                            lo[e] = pack_bf16(y[2 * e] - __uint_as_float(hi[e] << 16),
-                                              y[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
-                        }
-                        const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
-                        *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
-                        *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 gp = f2_unpack(acc[r >> 1][e]);
+                        y[e] = part ? (r & 1 ? gp.y : gp.x) : i0 + r == c0 + e ? 0.f : t[e];
                     }
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        hi[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+                        lo[e] = pack_bf16(y[2 * e] - __uint_as_float(hi[e] << 16),
+                                          y[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
+                    }
+                    const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
+                    *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
                 }
             }
             __syncthreads();
@@ -305,20 +346,23 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
 // ---------------------------------------------------------------- walk
 
-template <int VT>
+// A CTA runs two chains side by side, CW value columns each, on the same K, Q, T and G tiles: while the
+// epilogue warps of one pass over an accumulator, the MMAs of the other run.
+template <int CW>
 struct Walk {
-    static constexpr int NCG = VT / 16;                    // column groups of 16
-    static constexpr int EPI = 4 * NCG;                    // epilogue warps
-    static constexpr int THREADS = 64 + 32 * EPI;
+    static constexpr int NCH = 2;                          // chains
+    static constexpr int VT = NCH * CW;                    // value columns of the CTA
+    static constexpr int EPI = 4 * (CW / 16);              // epilogue warps per chain, 16 columns each
+    static constexpr int THREADS = 64 + 32 * NCH * EPI;
     static constexpr int STAGES = 2;
-    static constexpr uint32_t STAGE = 65536;               // [K; Q] 32 KB, [T; G] values and residues 16 KB each
-    static constexpr uint32_t SP = STAGES * STAGE;         // S parts: 128 rows, 3 VT columns (in blocks of 64)
-    static constexpr uint32_t BLOCKS = (3 * VT + 63) / 64;
-    static constexpr uint32_t YN = SP + BLOCKS * 16384;    // Y parts, then N parts: 64 rows
-    static constexpr uint32_t BAR = YN + BLOCKS * 8192;
-    static constexpr uint32_t NBAR = 2 * STAGES + 6;
+    static constexpr uint32_t STAGE = 65536;               // [K; Q] 32 KB, [T - I; G] values and residues 16 KB each
+    static constexpr uint32_t BLOCKS = (3 * CW + 63) / 64; // blocks of 64 columns that hold an operand's parts
+    static constexpr uint32_t SP = STAGES * STAGE;         // per chain: S parts, 128 rows
+    static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then N parts, 64 rows
+    static constexpr uint32_t BAR = YN + NCH * BLOCKS * 8192;
+    static constexpr uint32_t NBAR = 2 * STAGES + 6 * NCH;
     static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
-    static constexpr uint32_t TMEM_COLS = VT == 64 ? 512 : 256;   // X and then D, [E; F]: 3 VT each
+    static constexpr uint32_t TMEM_COLS = CW == 32 ? 512 : 256;   // per chain X and then D, [E; F]: 3 CW each
 };
 
 struct WalkParams {
@@ -332,17 +376,18 @@ struct WalkParams {
     Workspace w;
 };
 
-template <int VT, int KS>
-__global__ void __launch_bounds__(Walk<VT>::THREADS, 1)
+template <int CW, int KS>
+__global__ void __launch_bounds__(Walk<CW>::THREADS, 1)
 walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WalkParams p)
 {
-    using W = Walk<VT>;
-    constexpr int NST = W::STAGES;
+    using W = Walk<CW>;
+    constexpr int NST = W::STAGES, NCH = W::NCH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + W::BAR);
-    uint64_t *full = bars, *empty = bars + NST, *s_ready = bars + 2 * NST, *x_done = s_ready + 1, *y_ready = s_ready + 2,
-             *e_done = s_ready + 3, *n_ready = s_ready + 4, *d_done = s_ready + 5;
+    // per chain: S, Y and N written by the epilogue; X, [E; F] and D finished by the MMAs
+    uint64_t *full = bars, *empty = bars + NST, *s_ready = bars + 2 * NST, *x_done = s_ready + NCH, *y_ready = x_done + NCH,
+             *e_done = y_ready + NCH, *n_ready = e_done + NCH, *d_done = n_ready + NCH;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + W::NBAR), *abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bhv = blockIdx.y, b = bhv / p.NHV, bh = b * p.NH + (bhv % p.NHV) / (p.NHV / p.NH);
@@ -352,12 +397,14 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        mbar_init(s_ready, W::EPI);
-        mbar_init(x_done, 1);
-        mbar_init(y_ready, W::EPI / 2);
-        mbar_init(e_done, 1);
-        mbar_init(n_ready, W::EPI);
-        mbar_init(d_done, 1);
+        for (int h = 0; h < NCH; ++h) {
+            mbar_init(&s_ready[h], W::EPI);
+            mbar_init(&x_done[h], 1);
+            mbar_init(&y_ready[h], W::EPI / 2);
+            mbar_init(&e_done[h], 1);
+            mbar_init(&n_ready[h], W::EPI);
+            mbar_init(&d_done[h], 1);
+        }
         *abort_flag = 0u;
         fence_barrier_init();
         tma_prefetch(&tm_q);
@@ -393,113 +440,125 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if (lane == 0) {
             // A K-major (X, E) or MN-major (D), B MN-major; N = the parts' columns side by side, so that A is
             // read once for all of them
-            constexpr uint32_t IDX = idesc_bf16(128, 3 * VT, 0, 1), IDM = idesc_bf16(128, 2 * VT, 0, 1);
-            constexpr uint32_t IDD = idesc_bf16(128, 3 * VT, 1, 1);
+            constexpr uint32_t IDX = idesc_bf16(128, 3 * CW, 0, 1), IDM = idesc_bf16(128, 2 * CW, 0, 1);
+            constexpr uint32_t IDD = idesc_bf16(128, 3 * CW, 1, 1);
+            constexpr uint32_t BS = W::BLOCKS * 1024, BY = W::BLOCKS * 512;   // a chain's operands, 16-byte units
             const uint64_t bs = smem_desc(smem_u32(smem + W::SP), 16384, 1024);
             const uint64_t by = smem_desc(smem_u32(smem + W::YN), 8192, 1024);
             const uint64_t ak = smem_desc(smem_u32(smem), 16, 1024), at = smem_desc(smem_u32(smem) + 32768, 16, 1024);
             const uint64_t ad = smem_desc(smem_u32(smem), 16384, 1024);
-            for (int c = 0; c < nc; ++c) {
+            bool ok = true;
+            for (int c = 0; c < nc && ok; ++c) {
                 const int st = c % NST;
                 const uint64_t so = (uint64_t)st * (W::STAGE / 16);
                 const uint32_t ph = (uint32_t)c & 1u;
-                if (!mbar_wait(&full[st], (uint32_t)(c / NST) & 1u, wc)) break;
-                if (!mbar_wait(s_ready, ph, wc)) break;
-                tc_fence_after();
+                ok = mbar_wait(&full[st], (uint32_t)(c / NST) & 1u, wc);
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    mma_ss(tmem, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2), bs + (uint64_t)(k * 128), IDX, k > 0);
-                mma_commit(x_done);
-                if (!mbar_wait(y_ready, ph, wc)) break;
-                tc_fence_after();
+                for (int h = 0; h < NCH && ok; ++h) {
+                    if (!(ok = mbar_wait(&s_ready[h], ph, wc))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_ss(tmem + 3 * VT, at + so + (uint64_t)(k * 2), by + (uint64_t)(k * 128), IDX, k > 0);
+                    for (int k = 0; k < KS; ++k)
+                        mma_ss(tmem + h * 6 * CW, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+                               bs + (uint64_t)(h * BS + k * 128), IDX, k > 0);
+                    mma_commit(&x_done[h]);
+                }
 #pragma unroll
-                for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
-                    mma_ss(tmem + 3 * VT, at + so + (uint64_t)(1024 + k * 2), by + (uint64_t)(k * 128), IDM, 1);
-                mma_commit(e_done);
-                if (!mbar_wait(n_ready, ph, wc)) break;
-                tc_fence_after();
+                for (int h = 0; h < NCH && ok; ++h) {
+                    if (!(ok = mbar_wait(&y_ready[h], ph, wc))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)   // over X, which every warp has read
-                    mma_ss(tmem, ad + so + (uint64_t)(k * 128), by + (uint64_t)(k * 128), IDD, k > 0);
-                mma_commit(d_done);
-                mma_commit(&empty[st]);
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(tmem + h * 6 * CW + 3 * CW, at + so + (uint64_t)(k * 2), by + (uint64_t)(h * BY + k * 128), IDX, k > 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
+                        mma_ss(tmem + h * 6 * CW + 3 * CW, at + so + (uint64_t)(1024 + k * 2), by + (uint64_t)(h * BY + k * 128), IDM, 1);
+                    mma_commit(&e_done[h]);
+                }
+#pragma unroll
+                for (int h = 0; h < NCH && ok; ++h) {
+                    if (!(ok = mbar_wait(&n_ready[h], ph, wc))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)   // over X, which every warp has read
+                        mma_ss(tmem + h * 6 * CW, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 0);
+                    mma_commit(&d_done[h]);
+                }
+                if (ok) mma_commit(&empty[st]);
             }
         }
     } else {
-        const int quad = warp & 3, cg = (warp - 2) >> 2;
+        const int quad = warp & 3, h = (warp - 2) / W::EPI, cg = ((warp - 2) % W::EPI) >> 2;
         const int row = quad * 32 + lane, t = row & 63;        // TMEM lane; token of the chunk
         const bool krow = quad < 2;
-        const int col = blockIdx.x * VT + cg * 16;             // first of the thread's 16 value columns
-        const uint32_t tl = tmem_addr(tmem, quad * 32, cg * 16);
-        uint8_t *sp = smem + W::SP, *yn = smem + W::YN;
-        float s[16];                                           // row `row` of the state
+        const int col = blockIdx.x * W::VT + h * CW + cg * 16; // first of the thread's 16 value columns
+        const uint32_t tl = tmem_addr(tmem, quad * 32, h * 6 * CW + cg * 16);
+        uint8_t *sp = smem + W::SP + h * W::BLOCKS * 16384, *yn = smem + W::YN + h * W::BLOCKS * 8192;
+        uint64_t s[8];                                         // row `row` of the state, in pairs
         const size_t srow = ((size_t)bhv * p.DK + row) * p.DV + col;
         const int live_cols = min(16, p.DV - col);             // a multiple of 8, may be <= 0
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const float4 x = p.S0 && row < p.DK && e < live_cols ? *reinterpret_cast<const float4 *>(p.S0 + srow + e)
-                                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
-            s[e] = x.x; s[e + 1] = x.y; s[e + 2] = x.z; s[e + 3] = x.w;
+        for (int e = 0; e < 4; ++e) {
+            const float4 x = p.S0 && row < p.DK && 4 * e < live_cols ? *reinterpret_cast<const float4 *>(p.S0 + srow + 4 * e)
+                                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            s[2 * e] = f2_pack(x.x, x.y);
+            s[2 * e + 1] = f2_pack(x.z, x.w);
         }
-        uint4 vr[2];
-        float2 at = {}, al = {};
-        float btv = 0.f;
-        auto prefetch = [&](int c) {   // the token's value row, gates and write strength
+        for (int c = 0; c < nc; ++c) {
+            const uint32_t ph = (uint32_t)c & 1u;
+            const int len = min(CH, n - c * CH);
+            store_parts(sp, row, cg * 2, CW / 8, 128, s);
+            fence_proxy_async();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_ready[h]);
+            // the token's gates and value row: asked for here, they arrive while X is computed; a load in
+            // flight at one of the fences would hold it up.  The next chunk's row is brought to L2
             const int tok = c * CH + t;
             const float2 *A = p.w.A + ((size_t)bhv * p.w.NC + c) * 64;
-            at = A[t];
-            al = A[63];
-            btv = tok < n ? p.beta[(size_t)bhv * p.S + tok] : 0.f;
+            const float2 at = A[t];
+            const float ef = A[63].x, ea = at.x, eo = at.y;
             const __nv_bfloat16 *v = p.v + ((size_t)bhv * p.S + tok) * p.DV + col;
+            uint4 vr[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 vr[e] = krow && tok < n && 8 * e < live_cols ? *reinterpret_cast<const uint4 *>(v + 8 * e)
                                                              : make_uint4(0u, 0u, 0u, 0u);
-        };
-        if (nc > 0) prefetch(0);
-        for (int c = 0; c < nc; ++c) {
-            const uint32_t ph = (uint32_t)c & 1u;
-            const int len = min(CH, n - c * CH);
-            store_parts(sp, row, cg * 2, VT / 8, 128, s);
-            fence_proxy_async();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_ready);
-            const float ea = expf(at.x + at.y), eo = expf(gate_diff(al, at)) * btv, ef = expf(al.x + al.y);
-            float x[16];
-            if (!mbar_wait(x_done, ph, wc)) break;
+            if (krow && tok + CH < n && live_cols > 0)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (size_t)CH * p.DV));
+            uint64_t x[8], y[8];
+            if (!mbar_wait(&x_done[h], ph, wc)) break;
             tc_fence_after();
-            load_parts(tl, VT, x);
+            load_parts(tl, CW, x);
             if (krow) {
+                const uint64_t f = f2_pack(-ea, -ea);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 v2 = unpack_bf16((&vr[e >> 2].x)[e & 3]);
-                    x[2 * e] = t < len ? fmaf(-ea, x[2 * e], v2.x) : 0.f;
-                    x[2 * e + 1] = t < len ? fmaf(-ea, x[2 * e + 1], v2.y) : 0.f;
+                for (int e = 0; e < 8; ++e) x[e] = f2_fma(f, x[e], f2_from_bf16x2((&vr[e >> 2].x)[e & 3]));
+                if (t >= len) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = 0;
                 }
-                store_parts(yn, row, cg * 2, VT / 8, 64, x);
+                store_parts(yn, row, cg * 2, CW / 8, 64, x);
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(y_ready);
+                if (lane == 0) mbar_arrive(&y_ready[h]);
             } else {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(n_ready);   // X is read
+                if (lane == 0) mbar_arrive(&n_ready[h]);   // X is read
             }
-            if (c + 1 < nc) prefetch(c + 1);
-            float y[16];
-            if (!mbar_wait(e_done, ph, wc)) break;
+            if (!mbar_wait(&e_done[h], ph, wc)) break;
             tc_fence_after();
-            load_parts(tl + 3 * VT, VT, y);
+            load_parts(tl + 3 * CW, CW, y);
             if (krow) {
+                const uint64_t f = f2_pack(eo, eo);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = eo * (x[e] + y[e]);
-                store_parts(yn, row, cg * 2, VT / 8, 64, y);
-                if (cg == 0 && t >= len) {   // padding: its keys meet N's zeros, which NaN would survive
+                for (int e = 0; e < 8; ++e) y[e] = f2_mul(f, f2_add(x[e], y[e]));
+                store_parts(yn, row, cg * 2, CW / 8, 64, y);
+                if (h == 0 && cg == 0 && t >= len) {
+                    // padding: its keys meet N's zeros, which NaN would survive.  X of the other chain may still
+                    // read them (into lanes that nothing uses); its D is issued after this chain's N arrived
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         *reinterpret_cast<uint4 *>(smem + (c % NST) * W::STAGE + sw128_chunk(t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
@@ -507,34 +566,37 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(n_ready);
+                if (lane == 0) mbar_arrive(&n_ready[h]);
             } else if (t < len) {
                 __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + c * CH + t) * p.DV + col;
+                const uint64_t fe = f2_pack(ea, ea), fs = f2_pack(p.scale, p.scale);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (8 * e >= live_cols) break;
                     uint32_t z[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        z[u] = pack_bf16(p.scale * fmaf(ea, x[8 * e + 2 * u], y[8 * e + 2 * u]),
-                                         p.scale * fmaf(ea, x[8 * e + 2 * u + 1], y[8 * e + 2 * u + 1]));
+                    for (int u = 0; u < 4; ++u) z[u] = f2_to_bf16x2(f2_mul(fs, f2_fma(fe, x[4 * e + u], y[4 * e + u])));
                     *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(z[0], z[1], z[2], z[3]);
                 }
             }
-            if (!mbar_wait(d_done, ph, wc)) break;
+            if (!mbar_wait(&d_done[h], ph, wc)) break;
             tc_fence_after();
-            load_parts(tl, VT, y);
+            load_parts(tl, CW, y);
+            const uint64_t f = f2_pack(ef, ef);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] = fmaf(ef, s[e], y[e]);
+            for (int e = 0; e < 8; ++e) s[e] = f2_fma(f, s[e], y[e]);
         }
         if (p.S_final && row < p.DK) {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-                if (e < live_cols) *reinterpret_cast<float4 *>(p.S_final + srow + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+            for (int e = 0; e < 4; ++e)
+                if (4 * e < live_cols) {
+                    const float2 u = f2_unpack(s[2 * e]), v = f2_unpack(s[2 * e + 1]);
+                    *reinterpret_cast<float4 *>(p.S_final + srow + 4 * e) = make_float4(u.x, u.y, v.x, v.y);
+                }
         }
-        for (int r = n + (int)threadIdx.x - 64; r < p.S; r += 32 * W::EPI) {   // padding rows
-            __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + r) * p.DV + blockIdx.x * VT;
-            for (int e = 0; e < VT && (int)blockIdx.x * VT + e < p.DV; e += 8)
+        for (int r = n + (int)threadIdx.x - 64; r < p.S; r += W::THREADS - 64) {   // padding rows
+            __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + r) * p.DV + blockIdx.x * W::VT;
+            for (int e = 0; e < W::VT && (int)blockIdx.x * W::VT + e < p.DV; e += 8)
                 *reinterpret_cast<uint4 *>(o + e) = make_uint4(0u, 0u, 0u, 0u);
         }
     }
@@ -551,16 +613,16 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
 }
 
-template <int VT, int KS>
-cudaError_t launch_walk_vt(const Args &a, const Workspace &w, const CUtensorMap &mq, const CUtensorMap &mk, void *o,
+template <int CW, int KS>
+cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap &mq, const CUtensorMap &mk, void *o,
                            float *S_final)
 {
-    cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<VT, KS>, Walk<VT>::TOTAL);
+    cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<CW, KS>, Walk<CW>::TOTAL);
     if (e != cudaSuccess) return e;
     WalkParams p = {static_cast<const __nv_bfloat16 *>(a.v), a.beta, a.S0, a.lengths, static_cast<__nv_bfloat16 *>(o),
                     S_final, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w};
-    return launch_kernel(walk_tc_kernel<VT, KS>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(Walk<VT>::THREADS),
-                         Walk<VT>::TOTAL, a.stream, 1, mq, mk, p);
+    return launch_kernel(walk_tc_kernel<CW, KS>, dim3((a.DV + Walk<CW>::VT - 1) / Walk<CW>::VT, a.B * a.NHV), dim3(Walk<CW>::THREADS),
+                         Walk<CW>::TOTAL, a.stream, 1, mq, mk, p);
 }
 
 }  // namespace
@@ -580,8 +642,8 @@ cudaError_t launch_fwd_tc(const Args &a, const Workspace &w, void *o, float *S_f
     // a chunk takes longer the more columns a CTA has, so the columns are split while the GPU has SMs for it
     const bool narrow = (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
     if (a.DK > 64)
-        return narrow ? launch_walk_vt<32, 8>(a, w, mq, mk, o, S_final) : launch_walk_vt<64, 8>(a, w, mq, mk, o, S_final);
-    return narrow ? launch_walk_vt<32, 4>(a, w, mq, mk, o, S_final) : launch_walk_vt<64, 4>(a, w, mq, mk, o, S_final);
+        return narrow ? launch_walk_cw<16, 8>(a, w, mq, mk, o, S_final) : launch_walk_cw<32, 8>(a, w, mq, mk, o, S_final);
+    return narrow ? launch_walk_cw<16, 4>(a, w, mq, mk, o, S_final) : launch_walk_cw<32, 4>(a, w, mq, mk, o, S_final);
 }
 
 }  // namespace gdelta

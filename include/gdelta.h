@@ -103,7 +103,7 @@ mlstm_status gdelta_step(float *state, const void *q, const void *k, const void 
  *
  * workspace: gdelta_bwd_workspace_size() bytes, 256-byte aligned (the states at the
  * chunks' starts and their gradients, 8 DK DV bytes per chunk and value head, and
- * 12 DV bytes per token and value head make up most of it).
+ * 8 DV bytes per token and value head make up most of it).
  */
 size_t gdelta_bwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, mlstm_dtype dt);
 mlstm_status gdelta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,

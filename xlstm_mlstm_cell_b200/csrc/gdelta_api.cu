@@ -36,19 +36,22 @@ size_t plan(char *base, const Args &a, bool backward, Workspace *w)
         return p;
     };
     w->status = reinterpret_cast<uint32_t *>(take(sizeof(uint32_t)));
-    w->A = reinterpret_cast<float2 *>(take(sizeof(float2) * 64 * chunks));
-    if (!backward && tc_supported(a.bf16, a.DK, a.DV)) {
+    const bool tc = tc_supported(a.bf16, a.DK, a.DV);
+    if (tc) {
+        w->GB = reinterpret_cast<float2 *>(take(sizeof(float2) * 64 * chunks));
         w->TG = reinterpret_cast<uint8_t *>(take(32768 * chunks));
-        return off;
+    } else {
+        w->T = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
     }
-    w->T = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
-    w->P = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
+    if (!tc || backward) {
+        w->A = reinterpret_cast<float2 *>(take(sizeof(float2) * 64 * chunks));
+        w->P = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
+    }
     if (backward) {
         w->KK = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
         w->SC = reinterpret_cast<float *>(take(sizeof(float) * a.DK * a.DV * chunks));
         w->DSC = reinterpret_cast<float *>(take(sizeof(float) * a.DK * a.DV * chunks));
         w->E = reinterpret_cast<float *>(take(sizeof(float) * 64 * a.DV * chunks));
-        w->DU = reinterpret_cast<float *>(take(sizeof(float) * 64 * a.DV * chunks));
         w->DV = reinterpret_cast<float *>(take(sizeof(float) * 64 * a.DV * chunks));
     }
     return off;
@@ -124,9 +127,8 @@ mlstm_status gdelta_fwd(const void *q, const void *k, const void *v, const float
             e = launch_state_copy(S0, S_final, (size_t)B * NHV * DK * DV, a.stream);
         return cuda_status(e);
     }
-    if (w.TG) return cuda_status(launch_fwd_tc(a, w, o, S_final));
-    cudaError_t e = launch_prep(a, w, false);
-    if (e == cudaSuccess) e = launch_walk(a, w, o, S_final, false);
+    cudaError_t e = w.TG ? launch_prep_tc(a, w) : launch_prep(a, w, false);
+    if (e == cudaSuccess) e = w.TG ? launch_forward_tc(a, w, o, S_final) : launch_walk(a, w, o, S_final, false);
     return cuda_status(e);
 }
 
@@ -171,9 +173,10 @@ mlstm_status gdelta_bwd(const void *q, const void *k, const void *v, const float
             e = launch_state_copy(dS_final, dS0, (size_t)B * NHV * DK * DV, a.stream);
         return cuda_status(e);
     }
-    cudaError_t e = launch_prep(a, w, true);
-    if (e == cudaSuccess) e = launch_walk(a, w, nullptr, nullptr, true);
-    if (e == cudaSuccess) e = launch_reverse(a, w, d_o, dS_final, dv, dS0);
+    cudaError_t e = w.TG ? launch_prep_tc(a, w) : launch_prep(a, w, true);
+    if (e == cudaSuccess) e = w.TG ? launch_keep_tc(a, w) : launch_walk(a, w, nullptr, nullptr, true);
+    if (e == cudaSuccess)
+        e = w.TG ? launch_reverse_tc(a, w, d_o, dS_final, dv, dS0) : launch_reverse(a, w, d_o, dS_final, dv, dS0);
     if (e == cudaSuccess) e = launch_grad(a, w, d_o, dq, dk, dg, dbeta);
     return cuda_status(e);
 }

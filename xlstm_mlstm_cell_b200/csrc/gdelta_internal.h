@@ -29,25 +29,30 @@ struct Workspace {
     int NC;
     float2 *A;             // [BHV][NC][64] cumulative log gate of the chunk as value and residue
     float *T, *P, *KK;     // [BHV][NC][64][64] (row i, column j); KK the backward only
-    uint8_t *TG;           // tensor-core path: [BHV][NC] blocks of 32 KB, T and G as bf16 parts
+    float2 *GB;            // tensor-core path: [BHV][NC][64] e^a, and beta e^{a_64 - a}
+    uint8_t *TG;           // tensor-core path: [BHV][NC] blocks of 32 KB, T - I and G as bf16 parts
     // the backward
     float *SC, *DSC;       // [BHV][NC][DK][DV] states at the chunks' starts, gradients at their ends
-    float *E, *DU, *DV;    // [BHV][NC][64][DV]
+    float *E, *DV;         // [BHV][NC][64][DV]
 };
 
 // The chunk's own matrices: A, T, P and (with `kk`) KK.
 cudaError_t launch_prep(const Args &a, const Workspace &w, bool kk);
 // Forward walk: o and S_final (`keep` false), or the chunk-start states and E (`keep`).
 cudaError_t launch_walk(const Args &a, const Workspace &w, void *o, float *S_final, bool keep);
-// Reverse walk: dv, dS0 and the workspace's DSC, DU, DV.
+// Reverse walk: dv, dS0 and the workspace's DSC, DV.
 cudaError_t launch_reverse(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv,
                            float *dS0);
 // dq, dk, dg, dbeta of every chunk from the workspace.
 cudaError_t launch_grad(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
                         float *dbeta);
-// The forward pass on the tensor cores (workspace: A, TG), and the shapes it takes.
+// The same on the tensor cores, for the shapes that tc_supported names (workspace: GB, TG).
 bool tc_supported(bool bf16, int DK, int DV);
-cudaError_t launch_fwd_tc(const Args &a, const Workspace &w, void *o, float *S_final);
+cudaError_t launch_prep_tc(const Args &a, const Workspace &w);
+cudaError_t launch_forward_tc(const Args &a, const Workspace &w, void *o, float *S_final);
+cudaError_t launch_keep_tc(const Args &a, const Workspace &w);
+cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv,
+                              float *dS0);
 cudaError_t launch_state_copy(const float *S0, float *S_final, size_t n, cudaStream_t stream);
 
 struct StepArgs {

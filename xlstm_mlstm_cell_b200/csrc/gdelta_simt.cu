@@ -10,7 +10,7 @@
 //   grad     H = dV E^T,  dP = scale (dO E^T) diag(beta),  dA = -H diag(beta),
 //            Zq = scale e^a dO S^T,  Zk = -e^a dV S^T,  W = e^{a_64 - a} U dS'^T,
 //            dQ = Zq + (dP * D) K,  dK = Zk + W + (dP * D)^T Q + (dA * D + (dA * D)^T) K,
-//            dbeta_j = E_j . dU_j - sum_i KK_ij H_ij,
+//            dbeta_j = (e^{a_64 - a} W0 . K)_j + sum_i (scale P dO E^T - KK H)_ij,  W0 = E dS'^T,
 //            dg_t = sum_{i >= t} (Zq . Q + Zk . K)_i + sum_{j < t} (W . K)_j
 //                   + sum_{j < t <= i} (dP * P + dA * KK)_ij + e^{a_64} <S, dS'>
 // (dP * D masked to j <= i, dA * D to j < i.)  Only the walks are sequential over the chunks; their
@@ -339,7 +339,6 @@ reverse_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
                 float4 p = ld4(x + t * VT + j0);
                 p.x = scale * p.x + eo[t] * acc[r][0]; p.y = scale * p.y + eo[t] * acc[r][1];
                 p.z = scale * p.z + eo[t] * acc[r][2]; p.w = scale * p.w + eo[t] * acc[r][3];
-                if (in) st4(w.DU + (ch * 64 + t) * DV + col, p);
                 st4(y + t * VT + j0, make_float4(bt[t] * p.x, bt[t] * p.y, bt[t] * p.z, bt[t] * p.w));
             }
         }
@@ -406,7 +405,7 @@ reverse_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
 
 constexpr int LDK = 132;   // row stride of K and Q [64][128]
 constexpr size_t GRAD_SMEM =
-    sizeof(float) * (2 * 64 * LDK + 2 * 64 * LDT + 32 * (LDR + LDT + LDR + LDR) + 10 * 64 + 32) + sizeof(float2) * 64;
+    sizeof(float) * (2 * 64 * LDK + 2 * 64 * LDT + 32 * (LDR + LDT + LDR + LDR) + 5 * 64 + 32) + sizeof(float2) * 64;
 
 // The thread's 8 x 8 tile of a product with 128 columns: rows ra + {0..3}, rb + {0..3}, columns
 // 4 (tid & 15) + {0..3} and 64 more.
@@ -443,10 +442,8 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     float *ts = te + 32 * LDT;                    // [32][LDR] S transposed
     float *td = ts + 32 * LDR;                    // [32][LDR] dS' transposed
     float *ea = td + 32 * LDR, *eo = ea + 64, *bt = eo + 64, *zin = bt + 64, *zout = zin + 64;
-    float *red = zout + 64;                       // [4][64] + [32]
-    float *ssum = red + 256;
-    float *eu = ssum + 32;                        // [64] E . dU
-    float2 *a = reinterpret_cast<float2 *>(eu + 64);
+    float *ssum = zout + 64;                      // [32]
+    float2 *a = reinterpret_cast<float2 *>(ssum + 32);
     const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
     const int ty = tid >> 4, tx = tid & 15;
     griddep_wait();
@@ -489,7 +486,7 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         __syncthreads();
         // H = dV E^T and dO E^T (64 x 64 each), then Z = [dO; dV] S^T and W = E dS'^T
         float hx[8][4] = {}, z[8][8] = {}, wv[4][8] = {};
-        float sd = 0.f, euv = 0.f;
+        float sd = 0.f;
         for (int v0 = 0; v0 < DV; v0 += 32) {
             for (int i = tid; i < 64 * 8; i += 256) {
                 const int t = i & 63, j = (i >> 6) * 4;
@@ -497,8 +494,6 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 const float4 x = ok ? load4(d_o + (vrow + t) * DV + v0 + j) : zero4;
                 const float4 y = ok ? ld4(w.DV + (ch * 64 + t) * DV + v0 + j) : zero4;
                 const float4 e = ok ? ld4(w.E + (ch * 64 + t) * DV + v0 + j) : zero4;
-                const float4 u = ok ? ld4(w.DU + (ch * 64 + t) * DV + v0 + j) : zero4;
-                euv += e.x * u.x + e.y * u.y + e.z * u.z + e.w * u.w;   // t is the same in every round
                 const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w}, es[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -539,21 +534,20 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
             }
             __syncthreads();
         }
-        red[(tid >> 6) * 64 + (tid & 63)] = euv;
         sd = warp_sum(sd);
         if (lane == 0) ssum[tid >> 5] = sd;
         // the inter-chunk terms of dq and dk, and their products with q and k
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int t = 4 * ty + r;
-            const float fq = scale * ea[t], fk = -ea[t], fw = eo[t] * bt[t];
+            const float fq = scale * ea[t], fk = -ea[t], fw = eo[t];
             float zi = 0.f, zo = 0.f;
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const int d = s < 4 ? 4 * tx + s : 60 + 4 * tx + s;
                 const float x = fq * z[r][s], y = fk * z[4 + r][s], u = fw * wv[r][s];
                 acc[r][s] += x;
-                acc[4 + r][s] += y + u;
+                acc[4 + r][s] += y + bt[t] * u;
                 zi += x * qs[t * LDK + d] + y * ks[t * LDK + d];
                 zo += u * ks[t * LDK + d];
             }
@@ -570,8 +564,9 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int j = 4 * tx + s;
-                mp[i * LDT + j] = j < i ? bt[j] * (scale * hx[r][s] * pv[s] - hx[4 + r][s] * kv[s]) : 0.f;
-                ma[i * LDT + j] = j < i ? kv[s] * hx[4 + r][s] : 0.f;
+                const float z = scale * hx[r][s] * pv[s] - hx[4 + r][s] * kv[s];   // both zero above the diagonal
+                mp[i * LDT + j] = j < i ? bt[j] * z : 0.f;
+                ma[i * LDT + j] = z;
             }
         }
         __syncthreads();
@@ -582,18 +577,18 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
                 mp[tid * LDT + j] = s;
                 s += x;
             }
-        } else if (tid < 128) {   // column j of KK * H
+        } else if (tid < 128) {   // column j of the pairs
             const int j = tid - 64;
-            float s = 0.f;
-            for (int i = j + 1; i < 64; ++i) s += ma[i * LDT + j];
-            if (j < len) dbeta[vrow + j] = red[j] + red[64 + j] + red[128 + j] + red[192 + j] - s;
+            float s = zout[j];
+            for (int i = j; i < 64; ++i) s += ma[i * LDT + j];
+            if (j < len) dbeta[vrow + j] = s;
         }
         __syncthreads();
         if (tid < len) {
             const int t = tid;
             float s = 0.f;
             for (int i = t; i < 64; ++i) s += mp[i * LDT + t] + zin[i];
-            for (int j = 0; j < t; ++j) s += zout[j];
+            for (int j = 0; j < t; ++j) s += bt[j] * zout[j];
             float sdd = 0.f;
             for (int i = 0; i < 8; ++i) sdd += ssum[i];
             dg[vrow + t] = s + ea[63] * sdd;

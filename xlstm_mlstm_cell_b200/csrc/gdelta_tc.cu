@@ -1,22 +1,25 @@
-// gdelta_tc.cu -- the gated delta rule's forward pass on the 5th-generation tensor cores (tcgen05), for
-// bf16 inputs with 64 <= DK <= 128.
+// gdelta_tc.cu -- the gated delta rule on the 5th-generation tensor cores (tcgen05), for bf16 inputs with
+// 64 <= DK <= 128: the forward pass, and the backward's two walks.
 //
 // With S the state at a chunk's start (64 tokens) and a its cumulative log gates:
-//   prep  KK = strict_lower(D * K K^T), P = lower(D * Q K^T), T = (I + KK diag(beta))^-1, G = P diag(beta) T
-//   walk  X = [K; Q] S;  Y = V - e^a X_K;  [E - Y; F] = [T - I; G] Y;  O = scale (e^a X_Q + F);
-//         S' = e^{a_64} S + K^T (e^{a_64 - a} beta E)
-// G puts the scores' product with the chunk's corrections into the same MMA as T's, so a chunk is a chain
-// of three MMA groups, each followed by one pass of the epilogue warps over its accumulator.  Only that
-// chain is sequential; a CTA runs it for one value head and VT of its value columns.
+//   prep     KK = strict_lower(D * K K^T), P = lower(D * Q K^T), T = (I + KK diag(beta))^-1,
+//            G = scale P diag(beta) T
+//   forward  X = [K; Q] S;  Y = V - e^a X_K;  [E - Y; F] = [T - I; G] Y;  O = scale e^a X_Q + F;
+//            S' = e^{a_64} S + K^T (e^{a_64 - a} beta E)
+//   reverse  X = K dS';  Y = beta e^{a_64 - a} X;  dV - Y = (T - I)^T Y + G^T dO;
+//            dS = e^{a_64} dS' - K^T (e^a dV) + Q^T (scale e^a dO)
+// G puts the scores' product with the chunk's corrections into the same MMAs as T's, so a chunk is a chain
+// of three MMA groups in either direction, each followed by one pass of the epilogue warps over its
+// accumulator.  Only that chain is sequential; a CTA runs it for one value head and VT value columns.
 //
 // Operands.  K and Q are stacked in shared memory, 64 rows each, so that one M = 128 MMA serves both;
-// the same K tile, read MN-major, is the A operand of the state's update.  The fp32 operands S, Y, N =
-// e^{a_64 - a} beta E enter as three bf16 parts each, value, rounding residue and the residue's residue,
-// which hold all 24 bits, side by side along N: one MMA reads A once for all three, and the epilogue adds
-// the parts' columns.  T - I and G enter as two parts (rms error 2.7e-6 of the correction they carry); K, Q
-// are exact.  Without its unit diagonal T leaves Y itself out of the MMA: the threads that formed Y in fp32
-// add it to the result.  The fp32 state itself stays in the epilogue
-// threads' registers, a row (key element) of 16 columns each, and takes the update with fp32 additions.
+// the same tile, read MN-major, is the A operand of the state's update.  The fp32 operands S, Y and the
+// state update's enter as three bf16 parts each, which hold all 24 bits, side by side along N: one MMA
+// reads A once for all three, and the epilogue adds the parts' columns.  T - I and G enter as two parts,
+// value and rounding residue (rms error 2.7e-6 of the correction they carry); K, Q, dO are exact.  Without
+// its unit diagonal T leaves Y itself out of the MMA: the threads that formed Y in fp32 add it to the
+// result.  The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
+// each, and takes the update with fp32 additions.
 //
 // Roles: warp 0 one TMA thread, warp 1 the MMA thread (and the TMEM allocation), then 4 epilogue warps per
 // 16 value columns.  TMEM lane = token (K rows in lanes 0..63, Q rows in 64..127) or key element, so gates
@@ -167,7 +170,7 @@ MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync
 __global__ void __launch_bounds__(prep::THREADS, 4)
 prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const float *__restrict__ g, const float *__restrict__ beta, const int *__restrict__ lengths, int NH,
-               int NHV, int S, int DK, Workspace w)
+               int NHV, int S, int DK, float scale, Workspace w)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -225,6 +228,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
             if (warp == 0) {
                 float2 a0, a1;
+                if (w.A) chunk_gates(g + gt, len, lane, 1.0, w.A[ch * 64 + 2 * lane], w.A[ch * 64 + 2 * lane + 1]);
                 const float b0 = 2 * lane < len ? beta[gt + 2 * lane] : 0.f;
                 const float b1 = 2 * lane + 1 < len ? beta[gt + 2 * lane + 1] : 0.f;
                 chunk_gates_log2(g + gt, len, lane, a0, a1);
@@ -238,7 +242,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             const float4 ai = ga[i];
             // what the walk needs of the gates: e^a of the token, and beta e^{a_64 - a}
-            if (krow) w.A[ch * 64 + i] = make_float2(exp2f(ai.x + ai.y), ai.z * exp2f((ga[63].x - ai.x) + (ga[63].y - ai.y)));
+            if (krow) w.GB[ch * 64 + i] = make_float2(exp2f(ai.x + ai.y), ai.z * exp2f((ga[63].x - ai.x) + (ga[63].y - ai.y)));
             // rows and columns behind `len` hold whatever the padding does: selected away
             const int top = i < len ? (krow ? i : i + 1) : 0;
 #pragma unroll
@@ -258,13 +262,21 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         const int j = half * 16 + s;
                         const float4 aj = ga[j];
                         const bool on = j < top;   // selects, not a branch a column
-                        const float d = on ? (ai.x - aj.x) + (ai.y - aj.y) : 0.f, y = on ? x[s] * aj.z : 0.f;
+                        const float d = on ? (ai.x - aj.x) + (ai.y - aj.y) : 0.f, y = on ? x[s] : 0.f;
                         x[s] = exp2f(d) * y;
                     }
                 } else {
 #pragma unroll
                     for (int s = 0; s < 16; ++s) x[s] = 0.f;
                 }
+                if (w.KK) {   // the backward's KK and P
+                    float *dst = (krow ? w.KK : w.P) + ch * 4096 + i * 64 + half * 16;
+#pragma unroll
+                    for (int s = 0; s < 16; s += 4)
+                        *reinterpret_cast<float4 *>(dst + s) = make_float4(x[s], x[s + 1], x[s + 2], x[s + 3]);
+                }
+#pragma unroll
+                for (int s = 0; s < 16; ++s) x[s] *= ga[half * 16 + s].z;
                 if (krow) {
 #pragma unroll
                     for (int s = 0; s < 16; ++s) mc[(half * 16 + s) * LDT + i] = x[s];
@@ -303,7 +315,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             __syncthreads();
             prep::join<16>(mr, mc, (tid >> 4 & 1) * 32, tid & 15, tid < 32, [] { __syncthreads(); });
             prep::join<32>(mr, mc, 0, tid & 63, tid < 64, [] { __syncthreads(); });
-            // G = P diag(beta) T and [T - I; G] as two bf16 parts, each a swizzled tile of 128 rows of 64
+            // G = scale P diag(beta) T and [T - I; G] as two bf16 parts, each a swizzled tile of 128 rows of 64
             uint8_t *tg = w.TG + ch * 32768;
             const int i0 = (tid >> 4) * 8, c0 = (tid & 15) * 4;
             uint64_t acc[4][4];
@@ -318,7 +330,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float2 gp = f2_unpack(acc[r >> 1][e]);
-                        y[e] = part ? (r & 1 ? gp.y : gp.x) : i0 + r == c0 + e ? 0.f : t[e];
+                        y[e] = part ? scale * (r & 1 ? gp.y : gp.x) : i0 + r == c0 + e ? 0.f : t[e];
                     }
                     uint32_t hi[2], lo[2];
 #pragma unroll
@@ -348,7 +360,9 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
 // A CTA runs two chains side by side, CW value columns each, on the same K, Q, T and G tiles: while the
 // epilogue warps of one pass over an accumulator, the MMAs of the other run.
-template <int CW>
+enum Mode { FORWARD, KEEP, REVERSE };   // KEEP: the forward walk again, for the backward: states and E, no outputs
+
+template <int CW, int MODE>
 struct Walk {
     static constexpr int NCH = 2;                          // chains
     static constexpr int VT = NCH * CW;                    // value columns of the CTA
@@ -358,36 +372,39 @@ struct Walk {
     static constexpr uint32_t STAGE = 65536;               // [K; Q] 32 KB, [T - I; G] values and residues 16 KB each
     static constexpr uint32_t BLOCKS = (3 * CW + 63) / 64; // blocks of 64 columns that hold an operand's parts
     static constexpr uint32_t SP = STAGES * STAGE;         // per chain: S parts, 128 rows
-    static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then N parts, 64 rows
-    static constexpr uint32_t BAR = YN + NCH * BLOCKS * 8192;
-    static constexpr uint32_t NBAR = 2 * STAGES + 6 * NCH;
+    static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
+    static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : 64;   // (reverse: K's tokens, then Q's)
+    static constexpr uint32_t DO = YN + NCH * BLOCKS * YROWS * 128; // reverse: dO, 64 rows, the chains side by side
+    static constexpr uint32_t BAR = DO + (MODE == REVERSE ? 8192 : 0);
+    static constexpr uint32_t NBAR = 2 * STAGES + 7 * NCH;
     static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
     static constexpr uint32_t TMEM_COLS = CW == 32 ? 512 : 256;   // per chain X and then D, [E; F]: 3 CW each
 };
 
 struct WalkParams {
-    const __nv_bfloat16 *v;
-    const float *beta, *S0;
+    const __nv_bfloat16 *v;   // reverse: dO
+    const float *S0;          // reverse: dS_final
     const int *lengths;
-    __nv_bfloat16 *o;
-    float *S_final;
+    __nv_bfloat16 *o;         // reverse: dv
+    float *S_final;           // reverse: dS0
     int NH, NHV, S, DK, DV;
     float scale;
     Workspace w;
 };
 
-template <int CW, int KS>
-__global__ void __launch_bounds__(Walk<CW>::THREADS, 1)
+template <int CW, int KS, int MODE>
+__global__ void __launch_bounds__(Walk<CW, MODE>::THREADS, 1)
 walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WalkParams p)
 {
-    using W = Walk<CW>;
+    using W = Walk<CW, MODE>;
+    static_assert(MODE != REVERSE || CW == 16, "dO of both chains in one block of columns");
     constexpr int NST = W::STAGES, NCH = W::NCH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + W::BAR);
     // per chain: S, Y and N written by the epilogue; X, [E; F] and D finished by the MMAs
     uint64_t *full = bars, *empty = bars + NST, *s_ready = bars + 2 * NST, *x_done = s_ready + NCH, *y_ready = x_done + NCH,
-             *e_done = y_ready + NCH, *n_ready = e_done + NCH, *d_done = n_ready + NCH;
+             *e_done = y_ready + NCH, *n_ready = e_done + NCH, *d_done = n_ready + NCH, *o_ready = d_done + NCH;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + W::NBAR), *abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bhv = blockIdx.y, b = bhv / p.NHV, bh = b * p.NH + (bhv % p.NHV) / (p.NHV / p.NH);
@@ -404,6 +421,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&e_done[h], 1);
             mbar_init(&n_ready[h], W::EPI);
             mbar_init(&d_done[h], 1);
+            mbar_init(&o_ready[h], W::EPI / 2);
         }
         *abort_flag = 0u;
         fence_barrier_init();
@@ -425,15 +443,15 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (warp == 0) {
         if (lane == 0) {
             for (int c = 0; c < nc; ++c) {
-                const int st = c % NST;
+                const int st = c % NST, ci = MODE == REVERSE ? nc - 1 - c : c;
                 if (c >= NST && !mbar_wait(&empty[st], (uint32_t)(c / NST - 1) & 1u, wc)) break;
                 uint8_t *s = smem + st * W::STAGE;
                 mbar_arrive_expect_tx(&full[st], W::STAGE);
                 for (int kb = 0; kb < 2; ++kb) {
-                    tma_load_3d(s + kb * 16384, &tm_k, 64 * kb, c * CH, bh, &full[st]);
-                    tma_load_3d(s + kb * 16384 + 8192, &tm_q, 64 * kb, c * CH, bh, &full[st]);
+                    tma_load_3d(s + kb * 16384, &tm_k, 64 * kb, ci * CH, bh, &full[st]);
+                    tma_load_3d(s + kb * 16384 + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
                 }
-                bulk_load(s + 32768, p.w.TG + ((size_t)bhv * p.w.NC + c) * 32768, 32768, &full[st]);
+                bulk_load(s + 32768, p.w.TG + ((size_t)bhv * p.w.NC + ci) * 32768, 32768, &full[st]);
             }
         }
     } else if (warp == 1) {
@@ -442,9 +460,13 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // read once for all of them
             constexpr uint32_t IDX = idesc_bf16(128, 3 * CW, 0, 1), IDM = idesc_bf16(128, 2 * CW, 0, 1);
             constexpr uint32_t IDD = idesc_bf16(128, 3 * CW, 1, 1);
-            constexpr uint32_t BS = W::BLOCKS * 1024, BY = W::BLOCKS * 512;   // a chain's operands, 16-byte units
+            constexpr uint32_t BS = W::BLOCKS * 1024, BY = W::BLOCKS * W::YROWS * 8;   // a chain's operands, 16-byte units
+            // reverse: T^T and G^T, M = 64; the 64 M behind read what lies behind, into lanes that nothing uses
+            constexpr uint32_t IDT = idesc_bf16(128, 3 * CW, 1, 1), IDTM = idesc_bf16(128, 2 * CW, 1, 1), IDG = idesc_bf16(128, CW, 1, 1);
+            const uint64_t atm = smem_desc(smem_u32(smem) + 32768, 8192, 1024);
+            const uint64_t bo = MODE == REVERSE ? smem_desc(smem_u32(smem + W::DO), 8192, 1024) : 0;
             const uint64_t bs = smem_desc(smem_u32(smem + W::SP), 16384, 1024);
-            const uint64_t by = smem_desc(smem_u32(smem + W::YN), 8192, 1024);
+            const uint64_t by = smem_desc(smem_u32(smem + W::YN), W::YROWS * 128, 1024);
             const uint64_t ak = smem_desc(smem_u32(smem), 16, 1024), at = smem_desc(smem_u32(smem) + 32768, 16, 1024);
             const uint64_t ad = smem_desc(smem_u32(smem), 16384, 1024);
             bool ok = true;
@@ -462,17 +484,37 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         mma_ss(tmem + h * 6 * CW, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
                                bs + (uint64_t)(h * BS + k * 128), IDX, k > 0);
                     mma_commit(&x_done[h]);
+                    if (MODE == REVERSE) {
+                        if (!(ok = mbar_wait(&o_ready[h], ph, wc))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)   // G's rows lie 8 KB into the values' tile, and 16 KB further its residues'
+                            mma_ss(tmem + h * 6 * CW + 3 * CW, atm + so + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
+                                   bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, k > 0);
+                    }
                 }
 #pragma unroll
                 for (int h = 0; h < NCH && ok; ++h) {
                     if (!(ok = mbar_wait(&y_ready[h], ph, wc))) break;
                     tc_fence_after();
+                    const uint32_t de = tmem + h * 6 * CW + 3 * CW;
+                    if (MODE != REVERSE) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(tmem + h * 6 * CW + 3 * CW, at + so + (uint64_t)(k * 2), by + (uint64_t)(h * BY + k * 128), IDX, k > 0);
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(de, at + so + (uint64_t)(k * 2), by + (uint64_t)(h * BY + k * 128), IDX, k > 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
-                        mma_ss(tmem + h * 6 * CW + 3 * CW, at + so + (uint64_t)(1024 + k * 2), by + (uint64_t)(h * BY + k * 128), IDM, 1);
+                        for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
+                            mma_ss(de, at + so + (uint64_t)(1024 + k * 2), by + (uint64_t)(h * BY + k * 128), IDM, 1);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {   // the first part's columns onto G^T dO, the others from zero
+                            mma_ss(de, atm + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDG, 1);
+                            mma_ss(de + CW, atm + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128 + CW / 8), IDTM, k > 0);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(de, atm + so + (uint64_t)(1024 + k * 128), by + (uint64_t)(h * BY + k * 128), IDTM, 1);
+                    }
                     mma_commit(&e_done[h]);
                 }
 #pragma unroll
@@ -480,7 +522,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (!(ok = mbar_wait(&n_ready[h], ph, wc))) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)   // over X, which every warp has read
+                    for (int k = 0; k < (int)W::YROWS / 16; ++k)   // over X, which every warp has read
                         mma_ss(tmem + h * 6 * CW, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 0);
                     mma_commit(&d_done[h]);
                 }
@@ -493,7 +535,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const bool krow = quad < 2;
         const int col = blockIdx.x * W::VT + h * CW + cg * 16; // first of the thread's 16 value columns
         const uint32_t tl = tmem_addr(tmem, quad * 32, h * 6 * CW + cg * 16);
-        uint8_t *sp = smem + W::SP + h * W::BLOCKS * 16384, *yn = smem + W::YN + h * W::BLOCKS * 8192;
+        uint8_t *sp = smem + W::SP + h * W::BLOCKS * 16384, *yn = smem + W::YN + h * W::BLOCKS * W::YROWS * 128;
         uint64_t s[8];                                         // row `row` of the state, in pairs
         const size_t srow = ((size_t)bhv * p.DK + row) * p.DV + col;
         const int live_cols = min(16, p.DV - col);             // a multiple of 8, may be <= 0
@@ -506,76 +548,117 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = (uint32_t)c & 1u;
-            const int len = min(CH, n - c * CH);
+            const int ci = MODE == REVERSE ? nc - 1 - c : c, len = min(CH, n - ci * CH);
             store_parts(sp, row, cg * 2, CW / 8, 128, s);
             fence_proxy_async();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_ready[h]);
-            // the token's gates and value row: asked for here, they arrive while X is computed; a load in
-            // flight at one of the fences would hold it up.  The next chunk's row is brought to L2
-            const int tok = c * CH + t;
-            const float2 *A = p.w.A + ((size_t)bhv * p.w.NC + c) * 64;
-            const float2 at = A[t];
-            const float ef = A[63].x, ea = at.x, eo = at.y;
+            if (MODE != FORWARD && row < p.DK) {
+                float *keep = (MODE == KEEP ? p.w.SC : p.w.DSC) + (((size_t)bhv * p.w.NC + ci) * p.DK + row) * p.DV + col;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * e < live_cols) *reinterpret_cast<ulonglong2 *>(keep + 4 * e) = make_ulonglong2(s[2 * e], s[2 * e + 1]);
+            }
+            // the token's gates and its row of V (reverse: dO, the rows of Q's warps): asked for here, they
+            // arrive while X is computed; a load in flight at one of the fences would hold it up.  The next
+            // chunk's row is brought to L2
+            const int tok = ci * CH + t;
+            const float2 *GB = p.w.GB + ((size_t)bhv * p.w.NC + ci) * 64;
+            const float2 gt = GB[t];
+            const float ef = GB[63].x, ea = gt.x, eo = gt.y;
             const __nv_bfloat16 *v = p.v + ((size_t)bhv * p.S + tok) * p.DV + col;
+            const bool vrow = MODE == REVERSE ? !krow : krow;
             uint4 vr[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                vr[e] = krow && tok < n && 8 * e < live_cols ? *reinterpret_cast<const uint4 *>(v + 8 * e)
+                vr[e] = vrow && tok < n && 8 * e < live_cols ? *reinterpret_cast<const uint4 *>(v + 8 * e)
                                                              : make_uint4(0u, 0u, 0u, 0u);
-            if (krow && tok + CH < n && live_cols > 0)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (size_t)CH * p.DV));
+            const int ahead = MODE == REVERSE ? -CH : CH;
+            if (vrow && live_cols > 0 && tok + ahead >= 0 && tok + ahead < n)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(v + (ptrdiff_t)ahead * p.DV));
             uint64_t x[8], y[8];
+            if (MODE == REVERSE && !krow) {   // dO itself, and scale e^a dO behind the K tokens' rows
+#pragma unroll
+                for (int e = 0; e < 2; ++e) *reinterpret_cast<uint4 *>(smem + W::DO + sw128_chunk(t, h * (CW / 8) + cg * 2 + e, 64)) = vr[e];
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_ready[h]);
+                const uint64_t f = f2_pack(p.scale * ea, p.scale * ea);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = f2_mul(f, f2_from_bf16x2((&vr[e >> 2].x)[e & 3]));
+                store_parts(yn, row, cg * 2, CW / 8, W::YROWS, x);
+            }
             if (!mbar_wait(&x_done[h], ph, wc)) break;
             tc_fence_after();
-            load_parts(tl, CW, x);
+            uint8_t *kq = smem + (c % NST) * W::STAGE;
+            if (krow || MODE == FORWARD) load_parts(tl, CW, x);
             if (krow) {
-                const uint64_t f = f2_pack(-ea, -ea);
+                const float fx = MODE == REVERSE ? eo : -ea;
+                const uint64_t f = f2_pack(fx, fx);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = f2_fma(f, x[e], f2_from_bf16x2((&vr[e >> 2].x)[e & 3]));
+                for (int e = 0; e < 8; ++e)
+                    x[e] = MODE == REVERSE ? f2_mul(f, x[e]) : f2_fma(f, x[e], f2_from_bf16x2((&vr[e >> 2].x)[e & 3]));
                 if (t >= len) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = 0;
                 }
-                store_parts(yn, row, cg * 2, CW / 8, 64, x);
+                store_parts(yn, row, cg * 2, CW / 8, W::YROWS, x);
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&y_ready[h]);
             } else {
+                if (MODE == REVERSE) {
+                    if (h == 0 && cg == 0 && t >= len) {   // as for K below
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(64 + t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async();
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&n_ready[h]);   // X is read
+                if (lane == 0) mbar_arrive(&n_ready[h]);   // X is read (reverse: and Q's rows written)
             }
             if (!mbar_wait(&e_done[h], ph, wc)) break;
             tc_fence_after();
-            load_parts(tl + 3 * CW, CW, y);
+            if (krow || MODE == FORWARD) load_parts(tl + 3 * CW, CW, y);
             if (krow) {
-                const uint64_t f = f2_pack(eo, eo);
+                const float fn = MODE == REVERSE ? -ea : eo;
+                const uint64_t f = f2_pack(fn, fn);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = f2_mul(f, f2_add(x[e], y[e]));
-                store_parts(yn, row, cg * 2, CW / 8, 64, y);
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = f2_add(x[e], y[e]);   // E, or dV
+                    y[e] = f2_mul(f, x[e]);
+                }
+                store_parts(yn, row, cg * 2, CW / 8, W::YROWS, y);
                 if (h == 0 && cg == 0 && t >= len) {
                     // padding: its keys meet N's zeros, which NaN would survive.  X of the other chain may still
                     // read them (into lanes that nothing uses); its D is issued after this chain's N arrived
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        *reinterpret_cast<uint4 *>(smem + (c % NST) * W::STAGE + sw128_chunk(t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&n_ready[h]);
-            } else if (t < len) {
-                __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + c * CH + t) * p.DV + col;
-                const uint64_t fe = f2_pack(ea, ea), fs = f2_pack(p.scale, p.scale);
+                if (MODE != FORWARD) {
+                    float *keep = (MODE == KEEP ? p.w.E : p.w.DV) + (((size_t)bhv * p.w.NC + ci) * 64 + t) * p.DV + col;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * e < live_cols) *reinterpret_cast<ulonglong2 *>(keep + 4 * e) = make_ulonglong2(x[2 * e], x[2 * e + 1]);
+                }
+            }
+            if (MODE == FORWARD ? !krow && t < len : MODE == REVERSE && krow && t < len) {
+                __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + ci * CH + t) * p.DV + col;
+                const uint64_t fe = f2_pack(p.scale * ea, p.scale * ea);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if (8 * e >= live_cols) break;
                     uint32_t z[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) z[u] = f2_to_bf16x2(f2_mul(fs, f2_fma(fe, x[4 * e + u], y[4 * e + u])));
+                    for (int u = 0; u < 4; ++u)
+                        z[u] = f2_to_bf16x2(MODE == FORWARD ? f2_fma(fe, x[4 * e + u], y[4 * e + u]) : x[4 * e + u]);
                     *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(z[0], z[1], z[2], z[3]);
                 }
             }
@@ -586,7 +669,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = f2_fma(f, s[e], y[e]);
         }
-        if (p.S_final && row < p.DK) {
+        if (MODE != KEEP && p.S_final && row < p.DK) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (4 * e < live_cols) {
@@ -594,7 +677,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     *reinterpret_cast<float4 *>(p.S_final + srow + 4 * e) = make_float4(u.x, u.y, v.x, v.y);
                 }
         }
-        for (int r = n + (int)threadIdx.x - 64; r < p.S; r += W::THREADS - 64) {   // padding rows
+        for (int r = n + (int)threadIdx.x - 64; MODE != KEEP && r < p.S; r += W::THREADS - 64) {   // padding rows
             __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + r) * p.DV + blockIdx.x * W::VT;
             for (int e = 0; e < W::VT && (int)blockIdx.x * W::VT + e < p.DV; e += 8)
                 *reinterpret_cast<uint4 *>(o + e) = make_uint4(0u, 0u, 0u, 0u);
@@ -613,37 +696,63 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     }
 }
 
-template <int CW, int KS>
-cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap &mq, const CUtensorMap &mk, void *o,
-                           float *S_final)
+template <int CW, int KS, int MODE>
+cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap &mq, const CUtensorMap &mk, const void *v,
+                           const float *S0, void *o, float *S_final)
 {
-    cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<CW, KS>, Walk<CW>::TOTAL);
+    using W = Walk<CW, MODE>;
+    cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<CW, KS, MODE>, W::TOTAL);
     if (e != cudaSuccess) return e;
-    WalkParams p = {static_cast<const __nv_bfloat16 *>(a.v), a.beta, a.S0, a.lengths, static_cast<__nv_bfloat16 *>(o),
-                    S_final, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w};
-    return launch_kernel(walk_tc_kernel<CW, KS>, dim3((a.DV + Walk<CW>::VT - 1) / Walk<CW>::VT, a.B * a.NHV), dim3(Walk<CW>::THREADS),
-                         Walk<CW>::TOTAL, a.stream, 1, mq, mk, p);
+    WalkParams p = {static_cast<const __nv_bfloat16 *>(v), S0, a.lengths, static_cast<__nv_bfloat16 *>(o), S_final, a.NH,
+                    a.NHV, a.S, a.DK, a.DV, a.scale, w};
+    return launch_kernel(walk_tc_kernel<CW, KS, MODE>, dim3((a.DV + W::VT - 1) / W::VT, a.B * a.NHV), dim3(W::THREADS),
+                         W::TOTAL, a.stream, 1, mq, mk, p);
+}
+
+template <int MODE>
+cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const void *v, const float *S0, void *o, float *S_final)
+{
+    CUtensorMap mq, mk;
+    if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
+        return cudaErrorUnknown;
+    // a chunk takes longer the more columns a CTA has, so the columns are split while the GPU has SMs for it
+    const bool narrow = MODE == REVERSE || (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
+    if constexpr (MODE != REVERSE)
+        if (!narrow) return a.DK > 64 ? launch_walk_cw<32, 8, MODE>(a, w, mq, mk, v, S0, o, S_final)
+                                      : launch_walk_cw<32, 4, MODE>(a, w, mq, mk, v, S0, o, S_final);
+    return a.DK > 64 ? launch_walk_cw<16, 8, MODE>(a, w, mq, mk, v, S0, o, S_final)
+                     : launch_walk_cw<16, 4, MODE>(a, w, mq, mk, v, S0, o, S_final);
 }
 
 }  // namespace
 
 bool tc_supported(bool bf16, int DK, int DV) { return bf16 && DK >= 64 && DV >= 32; }
 
-cudaError_t launch_fwd_tc(const Args &a, const Workspace &w, void *o, float *S_final)
+cudaError_t launch_prep_tc(const Args &a, const Workspace &w)
 {
     CUtensorMap mq, mk;
     if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
         return cudaErrorUnknown;
-    cudaError_t e = ensure_dynamic_smem((const void *)prep_tc_kernel, prep::TOTAL);
+    const cudaError_t e = ensure_dynamic_smem((const void *)prep_tc_kernel, prep::TOTAL);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(prep_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, mq, mk, a.g,
-                      a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, w);
-    if (e != cudaSuccess) return e;
-    // a chunk takes longer the more columns a CTA has, so the columns are split while the GPU has SMs for it
-    const bool narrow = (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
-    if (a.DK > 64)
-        return narrow ? launch_walk_cw<16, 8>(a, w, mq, mk, o, S_final) : launch_walk_cw<32, 8>(a, w, mq, mk, o, S_final);
-    return narrow ? launch_walk_cw<16, 4>(a, w, mq, mk, o, S_final) : launch_walk_cw<32, 4>(a, w, mq, mk, o, S_final);
+    return launch_kernel(prep_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, mq, mk, a.g,
+                         a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.scale, w);
+}
+
+cudaError_t launch_forward_tc(const Args &a, const Workspace &w, void *o, float *S_final)
+{
+    return launch_walk_tc<FORWARD>(a, w, a.v, a.S0, o, S_final);
+}
+
+cudaError_t launch_keep_tc(const Args &a, const Workspace &w)
+{
+    return launch_walk_tc<KEEP>(a, w, a.v, a.S0, nullptr, nullptr);
+}
+
+cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv,
+                              float *dS0)
+{
+    return launch_walk_tc<REVERSE>(a, w, d_o, dS_final, dv, dS0);
 }
 
 }  // namespace gdelta

@@ -177,7 +177,8 @@ mlstm_status gdelta_bwd(const void *q, const void *k, const void *v, const float
     if (e == cudaSuccess) e = w.TG ? launch_keep_tc(a, w) : launch_walk(a, w, nullptr, nullptr, true);
     if (e == cudaSuccess)
         e = w.TG ? launch_reverse_tc(a, w, d_o, dS_final, dv, dS0) : launch_reverse(a, w, d_o, dS_final, dv, dS0);
-    if (e == cudaSuccess) e = launch_grad(a, w, d_o, dq, dk, dg, dbeta);
+    if (e == cudaSuccess)
+        e = w.TG ? launch_grad_tc(a, w, d_o, dq, dk, dg, dbeta) : launch_grad(a, w, d_o, dq, dk, dg, dbeta);
     return cuda_status(e);
 }
 

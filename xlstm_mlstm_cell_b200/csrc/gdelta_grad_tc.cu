@@ -1,0 +1,522 @@
+// gdelta_grad_tc.cu -- the gated delta rule's gradients of a chunk on tcgen05 (bf16 inputs, see
+// gdelta_simt.cu for the formulas): dq, dk, dg and dbeta from the states S at the chunk's start, their
+// gradients dS' at its end, E and dV, which the walks left in fp32.
+//
+//   HX = [dO; dV] E^T     Z = [dO; dV] S^T     W = E dS'^T       reduction over the value columns
+//   D += [dP; dA + dA^T] K + [0; dP^T] Q                         reduction over the tokens, all value heads
+//   dQ = scale e^a Z_dO + D,  dK = -e^a Z_dV + beta e^{a_64 - a} W + D
+//
+// dg and dbeta are fp32 outputs, so HX, Z and W take their fp32 operands as three bf16 parts (all 24
+// bits) and keep the six products of parts above 2^-24; D only reaches the bf16 dq and dk: two parts.
+//
+// One CTA per chunk and key head over its value heads; 64 value columns at a time the 256 threads bring
+// the operands from global memory into registers (the next group is asked for before the last one is
+// split), store their parts as swizzled tiles, and one thread issues the MMAs of a group while the next
+// is split.  TMEM lane = token (dO's rows, dq in lanes 0..63; dV's rows, dk in 64..127): a thread keeps
+// its row's 64 columns of dq or dk in registers across the heads.
+#include "gdelta_prep.cuh"
+#include "tc_common.cuh"
+#include "tc_fwd.h"
+
+namespace mlstm {
+namespace gdelta {
+namespace {
+
+using namespace tc;
+
+constexpr int THREADS = 256;
+constexpr int LDM = 65;                          // row stride of the 64 x 64 fp32 matrices (any row or column at once)
+constexpr uint32_t KQ = 0;                       // [2 blocks][128 rows][64]: K over Q
+constexpr uint32_t TA = 32768;                   // [dO; dV] values, [0; dV] residues, their residues: 16 KB each
+constexpr uint32_t TE = TA + 3 * 16384;          // E's three parts, 64 rows, 8 KB each
+constexpr uint32_t TS = TE + 3 * 8192;           // S's three parts, 128 rows, 16 KB each
+constexpr uint32_t TD = TS + 3 * 16384;          // dS' likewise
+// after the products over the value columns, over TA .. TD:
+constexpr uint32_t A1 = TA;                      // [dP; dA + dA^T] as two parts, 128 rows, 16 KB each
+constexpr uint32_t A2 = A1 + 32768;              // [0; dP^T]
+constexpr uint32_t MZ = A2 + 32768;              // fp32 [64][LDM]: scale P * dO E^T, later the pairs' prefix sums
+constexpr uint32_t MH = MZ + 64 * LDM * 4;       // -KK * H
+constexpr uint32_t MP = MH + 64 * LDM * 4;       // dP
+constexpr uint32_t MA = MP + 64 * LDM * 4;       // dA
+constexpr uint32_t GA = TD + 3 * 16384;          // [64] float4: cumulative gate (value, residue), beta, e^a
+constexpr uint32_t GO = GA + 1024;               // [64] e^{a_64 - a}
+constexpr uint32_t ZI = GO + 256;                // [2][2][64] shares of z_in by column half and row kind
+constexpr uint32_t ZO = ZI + 1024;               // [2][64] z_out by column half
+constexpr uint32_t SD = ZO + 512;                // [8] shares of <S, dS'>
+constexpr uint32_t BAR = SD + 32;
+constexpr uint32_t TOTAL = BAR + 48 + 1024;
+static_assert(MA + 64 * LDM * 4 <= GA, "the pairs' matrices fit over the operands");
+static_assert(TOTAL <= 232448, "one CTA's shared memory");
+
+// TMEM columns
+constexpr uint32_t CZ = 0, CW = 128, CH_ = 256, CD = 320;
+
+struct Params {
+    const __nv_bfloat16 *d_o;
+    const float *beta;
+    const int *lengths;
+    __nv_bfloat16 *dq, *dk;
+    float *dg, *dbeta;
+    int NH, NHV, S, DK, DV;
+    float scale;
+    Workspace w;
+};
+
+// Eight values as three bf16 parts (top, middle and last 8 significant bits), 16 bytes each.
+MLSTM_DEVINL void split3(const float4 &x, const float4 &y, uint4 (&p)[3])
+{
+    float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        uint32_t *o = &p[q].x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t u0 = __float_as_uint(v[2 * e]), u1 = __float_as_uint(v[2 * e + 1]);
+            o[e] = __byte_perm(u0, u1, 0x7632);
+            if (q < 2) {
+                v[2 * e] -= __uint_as_float(u0 & 0xffff0000u);
+                v[2 * e + 1] -= __uint_as_float(u1 & 0xffff0000u);
+            }
+        }
+    }
+}
+
+// 32 values of a row as two bf16 parts (value and rounding residue) into a tile of 128 rows; the residues
+// 16 KB behind.
+MLSTM_DEVINL void store2(uint8_t *tile, uint32_t row, uint32_t j0, const float (&x)[32])
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x0 = x[c * 8 + 2 * e], x1 = x[c * 8 + 2 * e + 1];
+            h[e] = pack_bf16(x0, x1);
+            l[e] = pack_bf16(x0 - __uint_as_float(h[e] << 16), x1 - __uint_as_float(h[e] & 0xffff0000u));
+        }
+        const uint32_t off = sw128_chunk(row, j0 + c, 128);
+        *reinterpret_cast<uint4 *>(tile + off) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(tile + 16384 + off) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+
+MLSTM_DEVINL void ld32(uint32_t taddr, float (&x)[32])
+{
+    uint32_t r[32];
+    tmem_ld32(taddr, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const Params p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    float4 *ga = reinterpret_cast<float4 *>(smem + GA);
+    float *go = reinterpret_cast<float *>(smem + GO), *zi = reinterpret_cast<float *>(smem + ZI);
+    float *zo = reinterpret_cast<float *>(smem + ZO), *sds = reinterpret_cast<float *>(smem + SD);
+    float *mz = reinterpret_cast<float *>(smem + MZ), *mh = reinterpret_cast<float *>(smem + MH);
+    float *mp = reinterpret_cast<float *>(smem + MP), *ma = reinterpret_cast<float *>(smem + MA);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + BAR);   // K and Q landed; products over the values; D
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 3), *abort_flag = tmem_slot + 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c = blockIdx.x, bh = blockIdx.y, b = bh / p.NH, group = p.NHV / p.NH;
+    const Workspace &w = p.w;
+    WaitCtx wc{abort_flag, w.status};
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(&bars[i], 1);
+        *abort_flag = 0u;
+        fence_barrier_init();
+        tma_prefetch(&tm_q);
+        tma_prefetch(&tm_k);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int full = min(CH, p.S - c * CH);
+    const int len = max(0, min(full, live_tokens(p.lengths, b, p.S) - c * CH));
+    const size_t row0 = (size_t)bh * p.S + c * CH;
+    for (int i = tid; i < (full - len) * (p.DK / 8); i += THREADS) {   // padding
+        const size_t at = (row0 + len) * p.DK + (size_t)i * 8;
+        *reinterpret_cast<uint4 *>(p.dq + at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(p.dk + at) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (int h = 0; h < group; ++h)
+        if (tid < full - len) {
+            const size_t gt = (size_t)(b * p.NHV + (bh % p.NH) * group + h) * p.S + c * CH + len + tid;
+            p.dg[gt] = 0.f;
+            p.dbeta[gt] = 0.f;
+        }
+
+    if (len > 0) {
+        if (tid == 0) {
+            mbar_arrive_expect_tx(&bars[0], 32768);
+            for (int kb = 0; kb < 2; ++kb) {
+                tma_load_3d(smem + KQ + kb * 16384, &tm_k, 64 * kb, c * CH, bh, &bars[0]);
+                tma_load_3d(smem + KQ + kb * 16384 + 8192, &tm_q, 64 * kb, c * CH, bh, &bars[0]);
+            }
+        }
+        __syncwarp();
+        const int quad = warp & 3, half = warp >> 2;
+        const int row = quad * 32 + lane, t = row & 63;     // TMEM lane; token
+        const bool top = quad < 2;                          // dO's rows and dq, else dV's and dk
+        const uint32_t tl = tmem_addr(tmem, quad * 32, 0);
+        const int nst = (p.DV + 63) / 64;
+        const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        uint64_t acc[32];                                   // 64 columns of the thread's row of dq or dk
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = 0;
+        // a thread's units of 8 values: row u0 + 32 k, columns c8 .. c8 + 7 of the 64
+        const int u0 = tid >> 3, c8 = (tid & 7) * 8;
+        // a wait of the whole CTA with one answer: all go on, or all leave
+        auto all_wait = [&](uint64_t *bar, uint32_t parity) { return __syncthreads_and(mbar_wait(bar, parity, wc)) != 0; };
+        bool ok = true;
+        uint32_t vphase = 0, dphase = 0;
+        constexpr uint32_t IDN = idesc_bf16(128, 128, 0, 0), IDH = idesc_bf16(128, 64, 0, 0), IDD = idesc_bf16(128, 128, 0, 1);
+        const uint64_t da = smem_desc(smem_u32(smem) + TA, 16, 1024), de = smem_desc(smem_u32(smem) + TE, 16, 1024);
+        const uint64_t ds = smem_desc(smem_u32(smem) + TS, 16, 1024), dd = smem_desc(smem_u32(smem) + TD, 16, 1024);
+        // the six products of parts: A's and B's part
+        constexpr int PA[6] = {0, 0, 0, 1, 1, 2}, PB[6] = {0, 1, 2, 0, 1, 0};
+
+        for (int h = 0; h < group && ok; ++h) {
+            const int bhv = b * p.NHV + (bh % p.NH) * group + h;
+            const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * p.S + c * CH;
+            const float *Sg = w.SC + ch * p.DK * p.DV, *Dg = w.DSC + ch * p.DK * p.DV;
+            const float *Eg = w.E + ch * 64 * p.DV, *Vg = w.DV + ch * 64 * p.DV;
+            const __nv_bfloat16 *Og = p.d_o + vrow * p.DV;
+            uint4 ro[2];
+            float4 rv[2][2], re[2][2], rs[4][2], rd[4][2];
+            auto load_ave = [&](int v0) {   // dO, dV, E
+                const int col = v0 + c8;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int r = u0 + 32 * k;
+                    const bool in = col < p.DV;
+                    ro[k] = in && r < len ? *reinterpret_cast<const uint4 *>(Og + (size_t)r * p.DV + col) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        rv[k][e] = in ? *reinterpret_cast<const float4 *>(Vg + (size_t)r * p.DV + col + 4 * e) : zero4;
+                        re[k][e] = in ? *reinterpret_cast<const float4 *>(Eg + (size_t)r * p.DV + col + 4 * e) : zero4;
+                    }
+                }
+            };
+            auto load_state = [&](const float *src, int v0, float4 (&x)[4][2]) {
+                const int col = v0 + c8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = u0 + 32 * k;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        x[k][e] = col < p.DV && r < p.DK ? *reinterpret_cast<const float4 *>(src + (size_t)r * p.DV + col + 4 * e) : zero4;
+                }
+            };
+            auto put_state = [&](uint32_t tile, const float4 (&x)[4][2]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint4 q[3];
+                    split3(x[k][0], x[k][1], q);
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        *reinterpret_cast<uint4 *>(smem + tile + e * 16384 + sw128_chunk(u0 + 32 * k, c8 / 8, 128)) = q[e];
+                }
+            };
+            load_ave(0);
+            load_state(Sg, 0, rs);
+            if (tid < 64) {
+                const float2 x = w.A[ch * 64 + tid], last = w.A[ch * 64 + 63];
+                ga[tid] = make_float4(x.x, x.y, tid < len ? p.beta[vrow + tid] : 0.f, expf(x.x + x.y));
+                go[tid] = expf(gate_diff(last, x));
+            }
+            float sd = 0.f;
+            for (int s = 0; s < nst; ++s) {
+                if (s > 0 && !(ok = all_wait(&bars[1], vphase++ & 1u))) break;   // the tiles are free
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t r = u0 + 32 * k, at = sw128_chunk(r, c8 / 8, 128), dn = sw128_chunk(64 + r, c8 / 8, 128);
+                    uint4 v[3], e[3];
+                    split3(rv[k][0], rv[k][1], v);
+                    split3(re[k][0], re[k][1], e);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        *reinterpret_cast<uint4 *>(smem + TA + q * 16384 + at) = q ? make_uint4(0u, 0u, 0u, 0u) : ro[k];
+                        *reinterpret_cast<uint4 *>(smem + TA + q * 16384 + dn) = v[q];
+                        *reinterpret_cast<uint4 *>(smem + TE + q * 8192 + sw128_chunk(r, c8 / 8, 64)) = e[q];
+                    }
+                }
+                load_state(Dg, s * 64, rd);
+                fence_proxy_async();
+                tc_fence_before();
+                __syncthreads();
+                if (tid == 0) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < 6; ++q)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(tmem + CH_, da + (uint64_t)(PA[q] * 1024 + k * 2), de + (uint64_t)(PB[q] * 512 + k * 2), IDH,
+                                   s + q + k > 0);
+                }
+                __syncwarp();
+                put_state(TS, rs);
+                fence_proxy_async();
+                __syncthreads();
+                if (tid == 0) {
+#pragma unroll
+                    for (int q = 0; q < 6; ++q)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(tmem + CZ, da + (uint64_t)(PA[q] * 1024 + k * 2), ds + (uint64_t)(PB[q] * 1024 + k * 2), IDN,
+                                   s + q + k > 0);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        sd += (rs[k][e].x * rd[k][e].x + rs[k][e].y * rd[k][e].y) + (rs[k][e].z * rd[k][e].z + rs[k][e].w * rd[k][e].w);
+                put_state(TD, rd);
+                if (s + 1 < nst) {
+                    load_ave((s + 1) * 64);
+                    load_state(Sg, (s + 1) * 64, rs);
+                }
+                fence_proxy_async();
+                __syncthreads();
+                if (tid == 0) {
+                    // E in rows 64..127; the rows in front of a part read what lies before it, into lanes nothing uses
+#pragma unroll
+                    for (int q = 0; q < 6; ++q)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(tmem + CW, de + (uint64_t)(PA[q] * 512 - 512 + k * 2), dd + (uint64_t)(PB[q] * 1024 + k * 2), IDN,
+                                   s + q + k > 0);
+                    mma_commit(&bars[1]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            sd = warp_sum(sd);
+            if (lane == 0) sds[warp] = sd;
+            if (h == 0) {   // K and Q: their padding rows would meet zeros, which NaN survives
+                if (!(ok = all_wait(&bars[0], 0))) break;
+                if (t >= len) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4 *>(smem + KQ + sw128_chunk(row, half * 8 + j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async();
+            }
+            // P's or KK's entries of the thread's row, asked for while the last products run
+            const int j0 = 32 * half;
+            const float *src = (top ? w.P : w.KK) + ch * 4096 + t * 64 + j0;
+            float pk[32];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float4 x = *reinterpret_cast<const float4 *>(src + 4 * e);
+                pk[4 * e] = x.x; pk[4 * e + 1] = x.y; pk[4 * e + 2] = x.z; pk[4 * e + 3] = x.w;
+            }
+            if (!(ok = all_wait(&bars[1], vphase++ & 1u))) break;
+            tc_fence_after();
+            const float4 gt = ga[t];
+            {   // the inter-chunk terms: 64 columns of Z and, for dk, of W, and their products with q and k
+                const float fz = top ? p.scale * gt.w : -gt.w, fw = go[t];
+                float zin = 0.f, zout = 0.f;
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    float z[32];
+                    ld32(tl + CZ + half * 64 + cc * 32, z);
+                    // row t of K (dk) or Q (dq)
+                    float qk[32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(smem + KQ + sw128_chunk(top ? 64 + t : t, half * 8 + cc * 4 + j, 128));
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = unpack_bf16(uu[e]);
+                            qk[8 * j + 2 * e] = f.x;
+                            qk[8 * j + 2 * e + 1] = f.y;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        zin = fmaf(z[e], qk[e], zin);
+                        zin = fmaf(z[e + 1], qk[e + 1], zin);
+                        acc[cc * 16 + e / 2] = f2_fma(f2_pack(fz, fz), f2_pack(z[e], z[e + 1]), acc[cc * 16 + e / 2]);
+                    }
+                    if (!top) {
+                        ld32(tl + CW + half * 64 + cc * 32, z);
+                        const float f = fw * gt.z;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            zout = fmaf(z[e], qk[e], zout);
+                            zout = fmaf(z[e + 1], qk[e + 1], zout);
+                            acc[cc * 16 + e / 2] = f2_fma(f2_pack(f, f), f2_pack(z[e], z[e + 1]), acc[cc * 16 + e / 2]);
+                        }
+                    }
+                }
+                zi[(half * 2 + (top ? 0 : 1)) * 64 + t] = t < len ? fz * zin : 0.f;
+                if (!top) zo[half * 64 + t] = t < len ? fw * zout : 0.f;
+            }
+            // the pairs: row t, columns j0 .. j0 + 31
+            float x[32], d[32];
+            ld32(tl + CH_ + j0, x);
+            if (dphase > 0 && !(ok = all_wait(&bars[2], (dphase - 1) & 1u))) break;   // the last head's D has read A1, A2
+            {
+                float *m1 = top ? mz : mh, *m2 = top ? mp : ma;
+                const float f = top ? p.scale : -1.f;
+                const int lim = top ? t : t - 1;   // P's columns j <= t, KK's j < t
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int j = j0 + e;
+                    const float4 gj = ga[j];
+                    const bool on = j <= lim;
+                    const float dif = on ? (gt.x - gj.x) + (gt.y - gj.y) : 0.f, v = on ? f * x[e] : 0.f;
+                    d[e] = expf(dif) * (gj.z * v);
+                    m1[t * LDM + j] = pk[e] * v;
+                    m2[t * LDM + j] = d[e];
+                }
+            }
+            if (top) {
+                store2(smem + A1, t, j0 / 8, d);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    *reinterpret_cast<uint4 *>(smem + A2 + sw128_chunk(t, j0 / 8 + j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(smem + A2 + 16384 + sw128_chunk(t, j0 / 8 + j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+            __syncthreads();
+            if (!top) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) d[e] += ma[(j0 + e) * LDM + t];
+                store2(smem + A1, row, j0 / 8, d);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) d[e] = mp[(j0 + e) * LDM + t];
+                store2(smem + A2, row, j0 / 8, d);
+            }
+            fence_proxy_async();
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc_fence_after();
+                const uint64_t a1 = smem_desc(smem_u32(smem) + A1, 16, 1024), a2 = smem_desc(smem_u32(smem) + A2, 16, 1024);
+                const uint64_t bk = smem_desc(smem_u32(smem) + KQ, 16384, 1024);
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        mma_ss(tmem + CD, a1 + (uint64_t)(q * 1024 + k * 2), bk + (uint64_t)(k * 128), IDD, h + q + k > 0);
+                        mma_ss(tmem + CD, a2 + (uint64_t)(q * 1024 + k * 2), bk + (uint64_t)(512 + k * 128), IDD, 1);
+                    }
+                mma_commit(&bars[2]);
+            }
+            __syncwarp();
+            ++dphase;
+            // dbeta_j = z_out_j + sum_i (mz + mh)_ij; a row's prefix sums over j < t', times beta, in place.
+            // Four threads a row or column, 16 entries each.
+            const int r = tid >> 2, s4 = tid & 3;
+            float z16[16], sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = s4 * 16 + e;
+                sum += mz[i * LDM + r] + mh[i * LDM + r];   // column r
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if (s4 == 0 && r < len) p.dbeta[vrow + r] = sum + zo[r] + zo[64 + r];
+            __syncthreads();
+            sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int j = s4 * 16 + e;
+                z16[e] = sum;
+                // the pair of a token with itself decays over no gate
+                sum += j < r ? ga[j].z * (mz[r * LDM + j] + mh[r * LDM + j]) : 0.f;
+            }
+            float before = 0.f;
+#pragma unroll
+            for (int o = 1; o < 4; ++o) {
+                const float y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (s4 >= o) before += y;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mz[r * LDM + s4 * 16 + e] = before + z16[e];
+            __syncthreads();
+            float dgt = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = s4 * 16 + e;   // rows i >= r, and tokens i on either side of r
+                if (i >= r) dgt += mz[i * LDM + r] + ((zi[i] + zi[64 + i]) + (zi[128 + i] + zi[192 + i]));
+                else dgt += ga[i].z * (zo[i] + zo[64 + i]);
+            }
+            dgt += __shfl_xor_sync(0xffffffffu, dgt, 1);
+            dgt += __shfl_xor_sync(0xffffffffu, dgt, 2);
+            if (s4 == 0 && r < len) {
+                float sum8 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum8 += sds[i];
+                p.dg[vrow + r] = dgt + ga[63].w * sum8;
+            }
+            // the next head's tiles lie over A1 and A2
+            if (h + 1 < group) {
+                if (!(ok = all_wait(&bars[2], (dphase - 1) & 1u))) break;
+                __syncthreads();
+            }
+        }
+        if (ok && all_wait(&bars[2], (dphase - 1) & 1u)) {
+            tc_fence_after();
+            __nv_bfloat16 *out = (top ? p.dq : p.dk) + (row0 + t) * p.DK + half * 64;
+#pragma unroll
+            for (int cc = 0; cc < 2; ++cc) {
+                float z[32];
+                ld32(tl + CD + half * 64 + cc * 32, z);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = f2_to_bf16x2(f2_add(acc[cc * 16 + 4 * j + e], f2_pack(z[8 * j + 2 * e], z[8 * j + 2 * e + 1])));
+                    if (t < len && half * 64 + cc * 32 + 8 * j < p.DK)
+                        *reinterpret_cast<uint4 *>(out + cc * 32 + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*reinterpret_cast<volatile uint32_t *>(abort_flag)) {
+        // a wait gave up: let MMAs and copies this CTA may still have in flight finish (bounded)
+        const unsigned long long tb = global_timer();
+        while (global_timer() - tb < 100000ull) { }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
+                           float *dbeta)
+{
+    CUtensorMap mq, mk;
+    if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
+        return cudaErrorUnknown;
+    const cudaError_t e = ensure_dynamic_smem((const void *)grad_tc_kernel, TOTAL);
+    if (e != cudaSuccess) return e;
+    Params p = {static_cast<const __nv_bfloat16 *>(d_o), a.beta, a.lengths, static_cast<__nv_bfloat16 *>(dq),
+                static_cast<__nv_bfloat16 *>(dk), dg, dbeta, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w};
+    return launch_kernel(grad_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(THREADS), TOTAL, a.stream, 1, mq, mk, p);
+}
+
+}  // namespace gdelta
+}  // namespace mlstm

@@ -53,6 +53,8 @@ cudaError_t launch_forward_tc(const Args &a, const Workspace &w, void *o, float 
 cudaError_t launch_keep_tc(const Args &a, const Workspace &w);
 cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv,
                               float *dS0);
+cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
+                           float *dbeta);
 cudaError_t launch_state_copy(const float *S0, float *S_final, size_t n, cudaStream_t stream);
 
 struct StepArgs {

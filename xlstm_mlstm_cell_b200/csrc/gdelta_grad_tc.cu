@@ -184,8 +184,8 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         constexpr uint32_t IDN = idesc_bf16(128, 128, 0, 0), IDH = idesc_bf16(128, 64, 0, 0), IDD = idesc_bf16(128, 128, 0, 1);
         const uint64_t da = smem_desc(smem_u32(smem) + TA, 16, 1024), de = smem_desc(smem_u32(smem) + TE, 16, 1024);
         const uint64_t ds = smem_desc(smem_u32(smem) + TS, 16, 1024), dd = smem_desc(smem_u32(smem) + TD, 16, 1024);
-        // the six products of parts: A's and B's part
-        constexpr int PA[6] = {0, 0, 0, 1, 1, 2}, PB[6] = {0, 1, 2, 0, 1, 0};
+        // the six products of parts, A's and B's, smallest first: the accumulation cuts bits off at the sum's size
+        constexpr int PA[6] = {0, 2, 1, 0, 1, 0}, PB[6] = {2, 0, 1, 1, 0, 0};
 
         for (int h = 0; h < group && ok; ++h) {
             const int bhv = b * p.NHV + (bh % p.NH) * group + h;

@@ -360,57 +360,59 @@ def slstm_batch_per_cluster(B, NH, DH, dtype) -> int:
 
 # ---------------------------------------------------------------- gated delta rule
 
-def _need(name, t, shape, dtype, device):
-    """Checks one tensor argument: the C ABI sees only its address."""
+def _need(name, t, shape, dtype, index):
+    """Checks one tensor argument (device ``index``): the C ABI sees only its address."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != device:
-        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    if t.get_device() != index:
+        raise ValueError("%s must be on cuda:%d, got %s" % (name, index, t.device))
+    raise ValueError("%s must be contiguous" % name)
 
 
-def _need_cuda(t):
-    if t.device.type != "cuda":
+def _cuda_index(t):
+    index = t.get_device()
+    if index < 0:
         raise ValueError("the tensors must be on a CUDA device, got %s" % t.device)
+    return index
 
 
-class _on:
-    """The device of the arguments as the current one, for the call alone, and the stream to use on it."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, device, stream):
-        self.index, self.stream = device.index, stream
 
-    def __enter__(self):
-        self.back = torch.cuda.current_device()
-        if self.back != self.index:
-            torch.cuda.set_device(self.index)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(self.index) if self.stream is None
-                               else self.stream.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.back != self.index:
-            torch.cuda.set_device(self.back)
+def _on(index, stream, call):
+    """``call(stream address)`` with the arguments' device as the current one, on ``stream`` or on the
+    device's current stream."""
+    current = torch._C._cuda_getDevice()
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if current == index:
+        return call(s)
+    torch.cuda.set_device(index)
+    try:
+        return call(s)
+    finally:
+        torch.cuda.set_device(current)
 
 
 def _gdelta_inputs(q, k, v, g, beta, lengths, step=False):
-    """Checks the delta rule's inputs; returns (dt, B, NH, NHV, S, DK, DV)."""
-    dt = _dt(q)
-    _need_cuda(q)
+    """Checks the delta rule's inputs; returns (dt, B, NH, NHV, S, DK, DV, device index)."""
+    dt, index = _dt(q), _cuda_index(q)
     if q.dim() != (3 if step else 4) or v.dim() != q.dim():
         raise ValueError("q, k and v must be %s" % ("[B, heads, D]" if step else "[B, heads, S, D]"))
-    B, NH, *T, DK = q.shape
-    NHV, DV = v.shape[1], v.shape[-1]
-    _need("q", q, q.shape, q.dtype, q.device)
-    _need("k", k, q.shape, q.dtype, q.device)
-    _need("v", v, (B, NHV, *T, DV), q.dtype, q.device)
-    _need("g", g, (B, NHV, *T), torch.float32, q.device)
-    _need("beta", beta, (B, NHV, *T), torch.float32, q.device)
+    shape, vshape = q.shape, v.shape
+    gates = (shape[0], vshape[1]) if step else (shape[0], vshape[1], shape[2])
+    _need("q", q, shape, q.dtype, index)
+    _need("k", k, shape, q.dtype, index)
+    _need("v", v, gates + (vshape[-1],), q.dtype, index)
+    _need("g", g, gates, torch.float32, index)
+    _need("beta", beta, gates, torch.float32, index)
     if lengths is not None:
-        _need("lengths", lengths, (B,), torch.int32, q.device)
-    return dt, B, NH, NHV, T[0] if T else 1, DK, DV
+        _need("lengths", lengths, (shape[0],), torch.int32, index)
+    return dt, shape[0], shape[1], vshape[1], 1 if step else shape[2], shape[-1], vshape[-1], index
 
 
 def gdelta_fwd_tensor_path(DK, DV, dtype) -> int:
@@ -425,15 +427,15 @@ def gdelta_workspace_size(B, NH, NHV, S, DK, DV, dtype, backward: bool = False) 
     return int(size(B, NH, NHV, S, DK, DV, dt))
 
 
-def _gdelta_workspace(workspace, sizes, dt, device, backward):
-    lib = load()
-    fn = "gdelta_bwd_workspace_size" if backward else "gdelta_fwd_workspace_size"
+def _gdelta_workspace(workspace, sizes, device, index, backward):
     if workspace is None:
-        n = int(getattr(lib, fn)(*sizes, dt))
+        lib = load()
+        fn = "gdelta_bwd_workspace_size" if backward else "gdelta_fwd_workspace_size"
+        n = int(getattr(lib, fn)(*sizes))
         if n == 0:
             raise MlstmError(fn, 2, lib)
         return torch.empty(n, dtype=torch.uint8, device=device)
-    _need("workspace", workspace, workspace.shape, torch.uint8, device)
+    _need("workspace", workspace, workspace.shape, torch.uint8, index)
     return workspace
 
 
@@ -448,23 +450,22 @@ def gdelta_fwd(q, k, v, g, beta, state=None, lengths=None, scale=None, o_out=Non
     DK ** -0.5.  The state is None with ``return_state=False``.
     """
     lib = load()
-    dt, B, NH, NHV, S, DK, DV = _gdelta_inputs(q, k, v, g, beta, lengths)
+    dt, B, NH, NHV, S, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, lengths)
     if state is not None:
-        _need("state", state, (B, NHV, DK, DV), torch.float32, q.device)
+        _need("state", state, (B, NHV, DK, DV), torch.float32, index)
     if o_out is None:
         o_out = torch.empty_like(v)
     else:
-        _need("o_out", o_out, v.shape, q.dtype, q.device)
+        _need("o_out", o_out, v.shape, q.dtype, index)
     if state_out is not None:
-        _need("state_out", state_out, (B, NHV, DK, DV), torch.float32, q.device)
+        _need("state_out", state_out, (B, NHV, DK, DV), torch.float32, index)
     elif return_state:
         state_out = torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device)
-    with _on(q.device, stream) as s:
-        workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV), dt, q.device, False)
-        _check("gdelta_fwd", lib.gdelta_fwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(lengths), dt, B, NH, NHV, S, DK, DV,
-            DK ** -0.5 if scale is None else scale, _ptr(state), _ptr(o_out), _ptr(state_out), _ptr(workspace),
-            workspace.numel(), s))
+    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, False)
+    _check("gdelta_fwd", _on(index, stream, lambda s: lib.gdelta_fwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), dt, B, NH, NHV, S, DK,
+        DV, DK ** -0.5 if scale is None else scale, _addr(state), o_out.data_ptr(), _addr(state_out),
+        workspace.data_ptr(), workspace.numel(), s)))
     return o_out, state_out
 
 
@@ -472,16 +473,15 @@ def gdelta_step(state, q, k, v, g, beta, scale=None, o_out=None, stream=None):
     """gdelta_step: one token of the gated delta rule; updates ``state`` ``[B, NHV, DK, DV]`` in place
     and returns o ``[B, NHV, DV]``.  q, k ``[B, NH, DK]``, v ``[B, NHV, DV]``, g, beta ``[B, NHV]``."""
     lib = load()
-    dt, B, NH, NHV, _, DK, DV = _gdelta_inputs(q, k, v, g, beta, None, step=True)
-    _need("state", state, (B, NHV, DK, DV), torch.float32, q.device)
+    dt, B, NH, NHV, _, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, None, step=True)
+    _need("state", state, (B, NHV, DK, DV), torch.float32, index)
     if o_out is None:
         o_out = torch.empty_like(v)
     else:
-        _need("o_out", o_out, v.shape, q.dtype, q.device)
-    with _on(q.device, stream) as s:
-        _check("gdelta_step", lib.gdelta_step(
-            _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), dt, B, NH, NHV, DK, DV,
-            DK ** -0.5 if scale is None else scale, _ptr(o_out), s))
+        _need("o_out", o_out, v.shape, q.dtype, index)
+    _check("gdelta_step", _on(index, stream, lambda s: lib.gdelta_step(
+        state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), dt, B, NH, NHV, DK,
+        DV, DK ** -0.5 if scale is None else scale, o_out.data_ptr(), s)))
     return o_out
 
 
@@ -491,27 +491,26 @@ def gdelta_bwd(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scal
     ``state`` (None: zero; ``dstate`` None: zero).  Returns ``(dq, dk, dv, dg, dbeta, dstate0)``, dstate0
     None without a ``state``; ``out`` may give those six tensors (the last one or None) to write into."""
     lib = load()
-    dt, B, NH, NHV, S, DK, DV = _gdelta_inputs(q, k, v, g, beta, lengths)
-    _need("do", do, v.shape, q.dtype, q.device)
+    dt, B, NH, NHV, S, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, lengths)
+    _need("do", do, v.shape, q.dtype, index)
     for name, t in (("state", state), ("dstate", dstate)):
         if t is not None:
-            _need(name, t, (B, NHV, DK, DV), torch.float32, q.device)
+            _need(name, t, (B, NHV, DK, DV), torch.float32, index)
     if out is None:
         out = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
                torch.empty_like(beta), None if state is None else torch.empty_like(state))
     else:
-        like = (q, k, v, g, beta)
-        for name, t, x in zip(("dq", "dk", "dv", "dg", "dbeta"), out, like):
-            _need(name, t, x.shape, x.dtype, q.device)
+        for name, t, x in zip(("dq", "dk", "dv", "dg", "dbeta"), out, (q, k, v, g, beta)):
+            _need(name, t, x.shape, x.dtype, index)
         if out[5] is not None:
-            _need("dstate0", out[5], (B, NHV, DK, DV), torch.float32, q.device)
+            _need("dstate0", out[5], (B, NHV, DK, DV), torch.float32, index)
     dq, dk, dv, dg, dbeta, dstate0 = out
-    with _on(q.device, stream) as s:
-        workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV), dt, q.device, True)
-        _check("gdelta_bwd", lib.gdelta_bwd(
-            _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(lengths), _ptr(state), _ptr(do), _ptr(dstate), dt, B,
-            NH, NHV, S, DK, DV, DK ** -0.5 if scale is None else scale, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-            _ptr(dbeta), _ptr(dstate0), _ptr(workspace), workspace.numel(), s))
+    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, True)
+    _check("gdelta_bwd", _on(index, stream, lambda s: lib.gdelta_bwd(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), _addr(state),
+        do.data_ptr(), _addr(dstate), dt, B, NH, NHV, S, DK, DV, DK ** -0.5 if scale is None else scale, dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dstate0), workspace.data_ptr(),
+        workspace.numel(), s)))
     return dq, dk, dv, dg, dbeta, dstate0
 
 
@@ -521,34 +520,33 @@ QKNORM_KINDS = {"rms": 0, "l2": 1}
 
 
 def _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions):
-    """Checks the norms' inputs; returns (dt, B, S, NHQ, NHK, D, RD, kind)."""
-    dt = _dt(q)
-    _need_cuda(q)
+    """Checks the norms' inputs; returns (dt, B, S, NHQ, NHK, D, RD, kind, device index)."""
+    dt, index = _dt(q), _cuda_index(q)
     if norm not in QKNORM_KINDS:
         raise ValueError("norm must be one of %s" % ", ".join(map(repr, QKNORM_KINDS)))
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B, S, heads, D]")
     B, S, NHQ, D = q.shape
     NHK = k.shape[2]
-    if k.shape != (B, S, NHK, D) or k.dtype != q.dtype or k.device != q.device:
-        raise ValueError("k must be [%d, %d, heads, %d] of %s on %s" % (B, S, D, q.dtype, q.device))
+    if k.shape != (B, S, NHK, D) or k.dtype != q.dtype or k.get_device() != index:
+        raise ValueError("k must be [%d, %d, heads, %d] of %s on %s" % (B, S, D, q.dtype, index))
     for name, t in (("q", q), ("k", k)):
         if t.numel() and t.stride(3) != 1:
             raise ValueError("the elements of a head of %s must be contiguous" % name)
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
         if t is not None:
-            _need(name, t, (D,), torch.float32, q.device)
+            _need(name, t, (D,), torch.float32, index)
     RD = 0
     if inv_freq is not None:
         RD = 2 * inv_freq.numel()
-        _need("inv_freq", inv_freq, (RD // 2,), torch.float32, q.device)
+        _need("inv_freq", inv_freq, (RD // 2,), torch.float32, index)
         if RD > D:
             raise ValueError("inv_freq must have at most D / 2 = %d frequencies, got %d" % (D // 2, RD // 2))
         if positions is not None:
-            _need("positions", positions, (B, S), torch.int32, q.device)
+            _need("positions", positions, (B, S), torch.int32, index)
     elif positions is not None:
         raise ValueError("positions without inv_freq")
-    return dt, B, S, NHQ, NHK, D, RD, QKNORM_KINDS[norm]
+    return dt, B, S, NHQ, NHK, D, RD, QKNORM_KINDS[norm], index
 
 
 def _strides(t):
@@ -568,19 +566,19 @@ def qknorm_fwd(q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: float
     0 .. S-1; pairs are (p, p + RD/2), or neighbours with ``interleaved``.
     """
     lib = load()
-    dt, B, S, NHQ, NHK, D, RD, kind = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
+    dt, B, S, NHQ, NHK, D, RD, kind, index = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
     if q_out is None:
         q_out = torch.empty((B, NHQ, S, D), dtype=q.dtype, device=q.device)
     else:
-        _need("q_out", q_out, (B, NHQ, S, D), q.dtype, q.device)
+        _need("q_out", q_out, (B, NHQ, S, D), q.dtype, index)
     if k_out is None:
         k_out = torch.empty((B, NHK, S, D), dtype=q.dtype, device=q.device)
     else:
-        _need("k_out", k_out, (B, NHK, S, D), q.dtype, q.device)
-    with _on(q.device, stream) as s:
-        _check("qknorm_fwd", lib.qknorm_fwd(
-            _ptr(q), _strides(q), _ptr(k), _strides(k), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq), _ptr(positions),
-            dt, B, S, NHQ, NHK, D, RD, kind, eps, 1 if interleaved else 0, _ptr(q_out), _ptr(k_out), s))
+        _need("k_out", k_out, (B, NHK, S, D), q.dtype, index)
+    _check("qknorm_fwd", _on(index, stream, lambda s: lib.qknorm_fwd(
+        q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq),
+        _addr(positions), dt, B, S, NHQ, NHK, D, RD, kind, eps, 1 if interleaved else 0, q_out.data_ptr(),
+        k_out.data_ptr(), s)))
     return q_out, k_out
 
 
@@ -590,27 +588,27 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm: str = "
     outputs (weight gradients None where the weight is).  ``out`` may give dq ``[B, S, NHQ, D]`` and dk to
     write into, such as slices of a fused projection's gradient (views that share no element)."""
     lib = load()
-    dt, B, S, NHQ, NHK, D, RD, kind = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
-    _need("dq_out", dq_out, (B, NHQ, S, D), q.dtype, q.device)
-    _need("dk_out", dk_out, (B, NHK, S, D), q.dtype, q.device)
+    dt, B, S, NHQ, NHK, D, RD, kind, index = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
+    _need("dq_out", dq_out, (B, NHQ, S, D), q.dtype, index)
+    _need("dk_out", dk_out, (B, NHK, S, D), q.dtype, index)
     if out is None:
         dq = torch.empty((B, S, NHQ, D), dtype=q.dtype, device=q.device)
         dk = torch.empty((B, S, NHK, D), dtype=q.dtype, device=q.device)
     else:
         dq, dk = out
         for name, t, x in (("dq", dq, q), ("dk", dk, k)):
-            if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or (t.numel() and t.stride(3) != 1):
+            if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != index or (t.numel() and t.stride(3) != 1):
                 raise ValueError("%s must be like its input, the elements of a head contiguous" % name)
     dwq = None if q_weight is None else torch.empty_like(q_weight)
     dwk = None if k_weight is None else torch.empty_like(k_weight)
-    with _on(q.device, stream) as s:
-        if workspace is None:
-            n = int(lib.qknorm_bwd_workspace_size(B, S, NHQ, NHK, D)) if (dwq is not None or dwk is not None) else 0
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-        else:
-            _need("workspace", workspace, workspace.shape, torch.uint8, q.device)
-        _check("qknorm_bwd", lib.qknorm_bwd(
-            _ptr(dq_out), _ptr(dk_out), _ptr(q), _strides(q), _ptr(k), _strides(k), _ptr(q_weight), _ptr(k_weight),
-            _ptr(inv_freq), _ptr(positions), dt, B, S, NHQ, NHK, D, RD, kind, eps, 1 if interleaved else 0, _ptr(dq),
-            _strides(dq), _ptr(dk), _strides(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace), workspace.numel(), s))
+    if workspace is None:
+        n = int(lib.qknorm_bwd_workspace_size(B, S, NHQ, NHK, D)) if (dwq is not None or dwk is not None) else 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    else:
+        _need("workspace", workspace, workspace.shape, torch.uint8, index)
+    _check("qknorm_bwd", _on(index, stream, lambda s: lib.qknorm_bwd(
+        dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), _addr(q_weight),
+        _addr(k_weight), _addr(inv_freq), _addr(positions), dt, B, S, NHQ, NHK, D, RD, kind, eps,
+        1 if interleaved else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(), _strides(dk), _addr(dwq), _addr(dwk),
+        workspace.data_ptr(), workspace.numel(), s)))
     return dq, dk, dwq, dwk

@@ -2,13 +2,22 @@
 //   r = 1 / sqrt(mean|sum(x^2) + eps),  z = r w x,  y = z with pairs of its first RD elements rotated;
 //   d = inverse rotation of dy,  dw = sum of d r x,  dx = r (w d - r^2 x mean|sum(w d x)).
 //
-// Bound by HBM: every vector is read once and written once (the backward reads two).  A CTA takes a few
-// tokens with all their query and key heads, so that the tokens' cosines and sines are formed once, in
-// shared memory, and serve every head; a group of lanes holds one vector in registers, each lane units of
-// VEC + VEC elements chosen so that both elements of a rotated pair sit in the same lane: no exchange but
-// the norm's sum over the group.  VEC is the widest vector that sizes, strides and pointers allow.
+// Bound by HBM: every vector is read once and written once (the backward reads two).  A group of lanes
+// takes a token and goes through its heads; each lane holds units of VEC + VEC elements of a vector, chosen
+// so that both elements of a rotated pair sit in the same lane, and the same pairs for every head: it forms
+// their cosines and sines once per token, in registers.  Nothing is exchanged but the norm's sum over the
+// group, so warps run on their own and hide one another's latency.  Where there are few tokens (a decode
+// step) a token's heads are dealt to several groups.  VEC is the widest vector that sizes, strides and
+// pointers allow, at most four elements.
+//
+// What it costs beyond the bytes is instructions and registers: packed fp32 pairs, one side per CTA and
+// four vectors loaded ahead took the forward pass over 16384 tokens of 16 + 16 heads of 128 (bf16, 268 MB)
+// from 106 to 64 us (4.2 TB/s) and the backward of 4 x 4096 tokens of 16 + 4 heads (252 MB) from 133 to
+// 72 us with the weights' sums (3.5 TB/s); two vectors ahead 68 and 73 us, tokens shared by a CTA with the
+// angles in shared memory 74 and 126 us.
 #include "common.cuh"
 #include "qknorm.h"
+#include "tc_common.cuh"
 
 #include <stdint.h>
 
@@ -18,8 +27,12 @@ namespace mlstm {
 namespace qknorm {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int SPAN = 8;      // VEC elements times units per lane: a vector of 512 is 32 lanes x 2 x 8
+using namespace tc;   // packed fp32 pairs
+
+constexpr int THREADS = 128;
+// SPAN: VEC elements times units per lane, 4 for vectors of up to 256 (32 lanes x 2 x 4), 8 beyond.  Wider
+// loads (8 bf16) with half the lanes took twice the registers and were slower for it.
+constexpr int AHEAD = 4;     // vectors a group loads before it works on the first of them
 
 struct Side {                // queries or keys
     const void *x, *dy;
@@ -34,27 +47,85 @@ struct Params {
     const float *inv_freq;
     const int *positions;
     float *part;             // [grid][2][D] partial weight gradients, or NULL
-    long long tokens;        // B * S
-    int B, S, D, RD, l2, TT, GL;
+    unsigned tokens;         // B * S
+    int B, S, D, RD, l2;
+    int GL, HS;              // lanes of a group; groups that share a token's heads
     float eps;
 };
 
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Vec { T e[VEC]; };
-
+// VEC elements as they lie in memory, in 32-bit words (a single bf16 in the low half of one): eight bf16
+// held as eight registers would cost the kernel half its warps.
 template <typename T, int VEC>
-MLSTM_DEVINL void load_vec(const T *p, float *x)
-{
-    const Vec<T, VEC> v = *reinterpret_cast<const Vec<T, VEC> *>(p);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = to_f32(v.e[i]);
-}
+struct Vec {
+    static constexpr int BYTES = (int)sizeof(T) * VEC;
+    uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
+};
 template <typename T, int VEC>
-MLSTM_DEVINL void store_vec(T *p, const float *x)
+MLSTM_DEVINL Vec<T, VEC> load_vec(const T *p)
 {
     Vec<T, VEC> v;
+    if constexpr (v.BYTES == 16) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        v.w[0] = u.x; v.w[1] = u.y; v.w[2] = u.z; v.w[3] = u.w;
+    } else if constexpr (v.BYTES == 8) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        v.w[0] = u.x; v.w[1] = u.y;
+    } else if constexpr (v.BYTES == 4) {
+        v.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+        v.w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+    return v;
+}
+
+// A unit's 2 VEC values as VEC packed pairs of floats in the order of memory; one element and its partner
+// make one pair where VEC is 1.  So a word holds a rotated pair (interleaved, or VEC 1), or two neighbours of
+// the same half.
+template <typename T, int VEC>
+MLSTM_DEVINL void widen(const Vec<T, VEC> (&v)[2], uint64_t (&x)[VEC])
+{
+    if constexpr (VEC == 1) {
+        if constexpr (sizeof(T) == 4) x[0] = f2_pack(__uint_as_float(v[0].w[0]), __uint_as_float(v[1].w[0]));
+        else x[0] = f2_pack(__uint_as_float(v[0].w[0] << 16), __uint_as_float(v[1].w[0] << 16));
+    } else {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v.e[i] = from_f32<T>(x[i]);
-    *reinterpret_cast<Vec<T, VEC> *>(p) = v;
+        for (int i = 0; i < VEC; ++i) {
+            const Vec<T, VEC> &u = v[i / (VEC / 2)];
+            const int j = i % (VEC / 2);
+            if constexpr (sizeof(T) == 4) x[i] = f2_pack(__uint_as_float(u.w[2 * j]), __uint_as_float(u.w[2 * j + 1]));
+            else x[i] = f2_from_bf16x2(u.w[j]);
+        }
+    }
+}
+template <typename T, int VEC>
+MLSTM_DEVINL void narrow(const uint64_t (&x)[VEC], Vec<T, VEC> (&v)[2])
+{
+    if constexpr (VEC == 1) {
+        const float2 f = f2_unpack(x[0]);
+        v[0].w[0] = sizeof(T) == 4 ? __float_as_uint(f.x) : bf16x2_bits(f.x, 0.f);
+        v[1].w[0] = sizeof(T) == 4 ? __float_as_uint(f.y) : bf16x2_bits(f.y, 0.f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            Vec<T, VEC> &u = v[i / (VEC / 2)];
+            const int j = i % (VEC / 2);
+            if constexpr (sizeof(T) == 4) {
+                const float2 f = f2_unpack(x[i]);
+                u.w[2 * j] = __float_as_uint(f.x);
+                u.w[2 * j + 1] = __float_as_uint(f.y);
+            } else {
+                u.w[j] = f2_to_bf16x2(x[i]);
+            }
+        }
+    }
+}
+template <typename T, int VEC>
+MLSTM_DEVINL void store_vec(T *p, const Vec<T, VEC> &v)
+{
+    if constexpr (v.BYTES == 16) *reinterpret_cast<uint4 *>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    else if constexpr (v.BYTES == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(v.w[0], v.w[1]);
+    else if constexpr (v.BYTES == 4) *reinterpret_cast<uint32_t *>(p) = v.w[0];
+    else *reinterpret_cast<uint16_t *>(p) = (uint16_t)v.w[0];
 }
 
 // A unit is VEC + VEC elements starting at o1 and o2.  Interleaved: 2 VEC neighbours.  Otherwise VEC
@@ -74,195 +145,245 @@ MLSTM_DEVINL void unit_offsets(int u, int D, int RD, int &o1, int &o2, bool &tur
     }
 }
 
-// Rotates a unit's pairs; cs holds the token's (cos, sin) of every pair.  sign -1 turns back.
+// Rotates a unit's VEC pairs by cs (cosines and sines); sign -1 turns back.
 template <int VEC, bool INTER>
-MLSTM_DEVINL void rotate(float *x, const float2 *cs, int o1, float sign)
+MLSTM_DEVINL void rotate(uint64_t (&x)[VEC], const float2 (&cs)[VEC], float sign)
 {
-    if (INTER && VEC > 1) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int e = 0; e + 1 < VEC; e += 2) {
-                const float2 t = cs[(o1 + h * VEC + e) / 2];
-                float &a = x[h * VEC + e], &b = x[h * VEC + e + 1];
-                const float c = t.x, s = sign * t.y, a0 = a;
-                a = a0 * c - b * s;
-                b = a0 * s + b * c;
-            }
-    } else {
+    if constexpr (INTER || VEC == 1) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const float2 t = cs[INTER ? o1 / 2 : o1 + e];
-            float &a = x[e], &b = x[VEC + e];
-            const float c = t.x, s = sign * t.y, a0 = a;
-            a = a0 * c - b * s;
-            b = a0 * s + b * c;
+            const float2 v = f2_unpack(x[e]);
+            const float s = sign * cs[e].y;
+            x[e] = f2_fma(x[e], f2_pack(cs[e].x, cs[e].x), f2_mul(f2_pack(v.y, v.x), f2_pack(-s, s)));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+            const uint64_t c = f2_pack(cs[2 * e].x, cs[2 * e + 1].x), a = x[e], b = x[VEC / 2 + e];
+            const uint64_t s = f2_pack(sign * cs[2 * e].y, sign * cs[2 * e + 1].y);
+            const uint64_t n = f2_pack(-sign * cs[2 * e].y, -sign * cs[2 * e + 1].y);
+            x[e] = f2_fma(a, c, f2_mul(b, n));
+            x[VEC / 2 + e] = f2_fma(b, c, f2_mul(a, s));
         }
     }
 }
 
-// The tile's cosines and sines.  The angle is formed in fp64 and brought to [-pi, pi] there, where an
-// fp32 sine is accurate to its own rounding.
-MLSTM_DEVINL void tile_angles(const Params &p, long long t0, int nt, float2 *cs, int tid)
+// A group's place: its lane, its token and what it needs of it.
+template <int VEC, int SPAN>
+struct Place {
+    int gl, units, hs;            // units: of a vector, 0 for a group without a token
+    unsigned b, t;
+    float2 cs[SPAN / VEC][VEC];   // of the lane's pairs
+};
+
+// The cosines and sines of the lane's pairs.  The angle is formed in fp64, in turns, and brought to half a
+// turn there, where an fp32 sine is accurate to its own rounding.
+template <int VEC, int SPAN, bool INTER>
+MLSTM_DEVINL void angles(const Params &p, unsigned tok, Place<VEC, SPAN> &g)
 {
-    const int half = p.RD / 2;
-    for (int i = tid; i < nt * half; i += THREADS) {
-        const int t = i / half, pr = i - t * half;
-        const long long tok = t0 + t;
-        const int pos = p.positions ? p.positions[tok] : (int)(tok % p.S);
-        const double ang = (double)pos * (double)p.inv_freq[pr];
-        const double red = ang - 6.283185307179586477 * rint(ang * 0.15915494309189533577);
-        float s, c;
-        sincosf((float)red, &s, &c);
-        cs[t * half + pr] = make_float2(c, s);
+    const double pos = (double)(p.positions ? p.positions[tok] : (int)g.t);
+#pragma unroll
+    for (int n = 0; n < SPAN / VEC; ++n) {
+        int o1, o2;
+        bool turn;
+        unit_offsets<VEC, INTER>(g.gl + n * p.GL, p.D, p.RD, o1, o2, turn);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            float s = 0.f, c = 1.f;
+            if (turn && g.gl + n * p.GL < g.units) {
+                const double turns = pos * (double)p.inv_freq[(INTER ? o1 / 2 : o1) + e] * 0.15915494309189533577;
+                sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+            }
+            g.cs[n][e] = make_float2(c, s);
+        }
     }
 }
 
-// One vector (or the vectors of one lane group) forward or backward.  gw: the lane's share of the
-// weight's gradient.
-template <typename T, int VEC, bool INTER, bool BWD>
-MLSTM_DEVINL void one_vector(const Params &p, const Side &sd, long long tok, int head, int gl, bool ok,
-                             const float2 *cs, float *gw)
+// What a lane has loaded of one vector: its units' values and, backward, the gradients of its outputs.
+template <typename T, int VEC, int SPAN, bool BWD>
+struct Held {
+    Vec<T, VEC> x[SPAN / VEC][2], d[BWD ? SPAN / VEC : 1][2];
+};
+
+// All of a token's heads of one side.  gw: the lane's share of the weight's gradient.
+template <typename T, int VEC, int SPAN, bool INTER, bool BWD>
+MLSTM_DEVINL void one_side(const Params &p, const Side &sd, const Place<VEC, SPAN> &g, uint64_t *gw)
 {
     constexpr int NU = SPAN / VEC;
-    const int units = p.D / 2 / VEC;
-    const int b = (int)(tok / p.S), t = (int)(tok % p.S);
-    const T *x = (const T *)sd.x + b * sd.xs.batch + t * sd.xs.token + head * sd.xs.head;
-    const size_t row = (((size_t)b * sd.heads + head) * p.S + t) * p.D;   // [B][heads][S][D]
-    const T *dy = (const T *)sd.dy + row;
-    float xv[NU][2 * VEC], dv[BWD ? NU : 1][2 * VEC];
-    float s = 0.f, xd = 0.f;
+    const T *x = (const T *)sd.x + g.b * sd.xs.batch + g.t * sd.xs.token;
+    const long long c0 = ((long long)g.b * sd.heads * p.S + g.t) * p.D, ch = (long long)p.S * p.D;   // contiguous tensors
+    const T *dy = (const T *)sd.dy + c0;
+    T *out = (T *)sd.out + (BWD ? g.b * sd.os.batch + g.t * sd.os.token : c0);
+    const long long oh = BWD ? sd.os.head : ch;
+    uint64_t w[NU][VEC];
+    bool has[NU];
+    int o1[NU], o2[NU];
+    bool turn[NU];
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
-        const int u = gl + n * p.GL;
-        if (!ok || u >= units) continue;
-        int o1, o2;
-        bool turn;
-        unit_offsets<VEC, INTER>(u, p.D, p.RD, o1, o2, turn);
-        load_vec<T, VEC>(x + o1, xv[n]);
-        load_vec<T, VEC>(x + o2, xv[n] + VEC);
-        if (BWD) {
-            load_vec<T, VEC>(dy + o1, dv[n]);
-            load_vec<T, VEC>(dy + o2, dv[n] + VEC);
-            if (turn) rotate<VEC, INTER>(dv[n], cs, o1, -1.f);
-        }
+        const int u = g.gl + n * p.GL;
+        has[n] = u < g.units;
+        unit_offsets<VEC, INTER>(u, p.D, p.RD, o1[n], o2[n], turn[n]);
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) {
-            s = fmaf(xv[n][e], xv[n][e], s);
-            if (BWD) {
-                const float w = sd.w ? sd.w[e < VEC ? o1 + e : o2 + e - VEC] : 1.f;
-                xd = fmaf(w * dv[n][e], xv[n][e], xd);
-            }
+        for (int e = 0; e < VEC; ++e) {
+            const int f0 = VEC == 1 ? o1[n] : e < VEC / 2 ? o1[n] + 2 * e : o2[n] + 2 * e - VEC;
+            const int f1 = VEC == 1 ? o2[n] : f0 + 1;
+            w[n][e] = sd.w && has[n] ? f2_pack(sd.w[f0], sd.w[f1]) : f2_pack(1.f, 1.f);
         }
-    }
-    for (int o = p.GL / 2; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (BWD) xd += __shfl_xor_sync(0xffffffffu, xd, o);
     }
     const float inv_n = p.l2 ? 1.f : 1.f / (float)p.D;
-    const float r = 1.f / sqrtf(fmaf(s, inv_n, p.eps));
-    const float back = BWD ? r * r * (xd * inv_n) : 0.f;
-    T *out = (T *)sd.out + (BWD ? b * sd.os.batch + t * sd.os.token + head * sd.os.head : (long long)row);
+    const int rounds = (sd.heads + p.HS * AHEAD - 1) / (p.HS * AHEAD);   // the same for every group of the warp
+    int head = g.hs;
+    x += head * sd.xs.head;
+    dy += head * ch;
+    out += head * oh;
+    const long long xstep = p.HS * sd.xs.head, cstep = p.HS * ch, ostep = p.HS * oh;
+#pragma unroll 1
+    for (int round = 0; round < rounds; ++round) {
+        Held<T, VEC, SPAN, BWD> v[AHEAD];
 #pragma unroll
-    for (int n = 0; n < NU; ++n) {
-        const int u = gl + n * p.GL;
-        if (!ok || u >= units) continue;
-        int o1, o2;
-        bool turn;
-        unit_offsets<VEC, INTER>(u, p.D, p.RD, o1, o2, turn);
+        for (int k = 0; k < AHEAD; ++k) {
 #pragma unroll
-        for (int e = 0; e < 2 * VEC; ++e) {
-            const float w = sd.w ? sd.w[e < VEC ? o1 + e : o2 + e - VEC] : 1.f;
-            if (BWD) {
-                gw[n * 2 * VEC + e] = fmaf(dv[n][e], r * xv[n][e], gw[n * 2 * VEC + e]);
-                xv[n][e] = r * (w * dv[n][e] - back * xv[n][e]);
-            } else {
-                xv[n][e] *= r * w;
-            }
+            for (int n = 0; n < NU; ++n)
+                if (has[n] && head + k * p.HS < sd.heads) {
+                    v[k].x[n][0] = load_vec<T, VEC>(x + o1[n]);
+                    v[k].x[n][1] = load_vec<T, VEC>(x + o2[n]);
+                    if (BWD) {
+                        v[k].d[n][0] = load_vec<T, VEC>(dy + o1[n]);
+                        v[k].d[n][1] = load_vec<T, VEC>(dy + o2[n]);
+                    }
+                }
+            x += xstep;
+            if (BWD) dy += cstep;
         }
-        if (!BWD && turn) rotate<VEC, INTER>(xv[n], cs, o1, 1.f);
-        store_vec<T, VEC>(out + o1, xv[n]);
-        store_vec<T, VEC>(out + o2, xv[n] + VEC);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const bool on = head < sd.heads;
+            uint64_t xv[NU][VEC], d[BWD ? NU : 1][VEC], gwd[BWD ? NU : 1][VEC], s2 = 0, xd2 = 0;   // gwd: d without the weight
+#pragma unroll
+            for (int n = 0; n < NU; ++n) {
+                if (!has[n] || !on) continue;
+                widen<T, VEC>(v[k].x[n], xv[n]);
+                if (BWD) {
+                    widen<T, VEC>(v[k].d[n], d[n]);
+                    if (turn[n]) rotate<VEC, INTER>(d[n], g.cs[n], -1.f);
+                }
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    s2 = f2_fma(xv[n][e], xv[n][e], s2);
+                    if (BWD) {
+                        gwd[n][e] = d[n][e];
+                        d[n][e] = f2_mul(w[n][e], d[n][e]);
+                        xd2 = f2_fma(d[n][e], xv[n][e], xd2);
+                    }
+                }
+            }
+            float s = f2_unpack(s2).x + f2_unpack(s2).y, xd = f2_unpack(xd2).x + f2_unpack(xd2).y;
+            for (int o = p.GL / 2; o > 0; o >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (BWD) xd += __shfl_xor_sync(0xffffffffu, xd, o);
+            }
+            const float r = rsqrtf(fmaf(s, inv_n, p.eps));
+            const float back = BWD ? -r * r * r * (xd * inv_n) : 0.f;
+            const uint64_t r2 = f2_pack(r, r), back2 = f2_pack(back, back);
+#pragma unroll
+            for (int n = 0; n < NU; ++n) {
+                if (!has[n] || !on) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    if (BWD) {
+                        gw[n * VEC + e] = f2_fma(gwd[n][e], f2_mul(r2, xv[n][e]), gw[n * VEC + e]);
+                        xv[n][e] = f2_fma(r2, d[n][e], f2_mul(back2, xv[n][e]));
+                    } else {
+                        xv[n][e] = f2_mul(xv[n][e], f2_mul(r2, w[n][e]));
+                    }
+                }
+                if (!BWD && turn[n]) rotate<VEC, INTER>(xv[n], g.cs[n], 1.f);
+                Vec<T, VEC> y[2];
+                narrow<T, VEC>(xv[n], y);
+                store_vec<T, VEC>(out + o1[n], y[0]);
+                store_vec<T, VEC>(out + o2[n], y[1]);
+            }
+            head += p.HS;
+            out += ostep;
+        }
     }
 }
 
-template <typename T, int VEC, bool INTER, bool BWD>
-__global__ void __launch_bounds__(THREADS)
-qknorm_kernel(const Params p)
+// blockIdx.y: queries or keys.
+template <typename T, int VEC, int SPAN, bool INTER, bool BWD>
+__global__ void __launch_bounds__(THREADS, BWD ? 4 : 6)
+qknorm_kernel(const __grid_constant__ Params p)
 {
-    extern __shared__ __align__(16) float2 cs[];   // [TT][RD / 2], at the end [groups][D] partial sums
-    const int tid = threadIdx.x, gl = tid % p.GL, grp = tid / p.GL, groups = THREADS / p.GL;
+    extern __shared__ __align__(16) float red[];   // backward: [groups][D]
+    const int tid = threadIdx.x, grp = tid / p.GL, groups = THREADS / p.GL;
+    const Side &sd = p.side[blockIdx.y];
+    Place<VEC, SPAN> g;
+    g.gl = tid % p.GL;
     griddep_wait();
     griddep_launch_dependents();
-    float gw[BWD ? 2 : 1][BWD ? 2 * SPAN : 1] = {};
-    const long long ntiles = (p.tokens + p.TT - 1) / p.TT;
-    for (long long tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-        const long long t0 = tile * p.TT;
-        const int nt = (int)min((long long)p.TT, p.tokens - t0);
-        if (p.RD) {
-            __syncthreads();
-            tile_angles(p, t0, nt, cs, tid);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int sdi = 0; sdi < 2; ++sdi) {
-            const Side &sd = p.side[sdi];
-            const int rows = nt * sd.heads;
-            for (int r0 = 0; r0 < rows; r0 += groups) {   // whole warps stay together for the sums
-                const int r = r0 + grp;
-                const bool ok = r < rows;
-                const int t = ok ? r / sd.heads : 0, head = ok ? r - t * sd.heads : 0;
-                one_vector<T, VEC, INTER, BWD>(p, sd, t0 + t, head, gl, ok, cs + t * (p.RD / 2), gw[BWD ? sdi : 0]);
-            }
-        }
+    uint64_t gw[BWD ? SPAN : 1] = {};
+    const unsigned long long items = (unsigned long long)p.tokens * p.HS, step = (unsigned long long)gridDim.x * groups;
+    // whole warps stay together for the sums: a group without an item goes along without a unit
+#pragma unroll 1
+    for (unsigned long long i0 = (unsigned long long)blockIdx.x * groups; i0 < items; i0 += step) {
+        const unsigned long long i = i0 + grp;
+        const bool on = i < items;
+        const unsigned tok = on ? (unsigned)(p.HS == 1 ? i : i / p.HS) : 0u;
+        g.units = on ? p.D / 2 / VEC : 0;
+        g.hs = on && p.HS > 1 ? (int)(i - (unsigned long long)tok * p.HS) : 0;
+        g.b = tok / (unsigned)p.S;
+        g.t = tok - g.b * (unsigned)p.S;
+        if (p.RD) angles<VEC, SPAN, INTER>(p, tok, g);
+        one_side<T, VEC, SPAN, INTER, BWD>(p, sd, g, gw);
     }
-    if (BWD && p.part) {   // the groups' shares of the weights' gradients, added in order
-        float *red = reinterpret_cast<float *>(cs);
+    if (BWD && p.part) {   // the groups' shares of the weight's gradient, added in order
         const int units = p.D / 2 / VEC;
-        for (int sdi = 0; sdi < 2; ++sdi) {
-            __syncthreads();
 #pragma unroll
-            for (int n = 0; n < SPAN / VEC; ++n) {
-                const int u = gl + n * p.GL;
-                if (u >= units) continue;
-                int o1, o2;
-                bool turn;
-                unit_offsets<VEC, INTER>(u, p.D, p.RD, o1, o2, turn);
+        for (int n = 0; n < SPAN / VEC; ++n) {
+            const int u = g.gl + n * p.GL;
+            if (u >= units) continue;
+            int o1, o2;
+            bool turn;
+            unit_offsets<VEC, INTER>(u, p.D, p.RD, o1, o2, turn);
 #pragma unroll
-                for (int e = 0; e < 2 * VEC; ++e)
-                    red[grp * p.D + (e < VEC ? o1 + e : o2 + e - VEC)] = gw[BWD ? sdi : 0][BWD ? n * 2 * VEC + e : 0];
+            for (int e = 0; e < VEC; ++e) {
+                const float2 f = f2_unpack(gw[BWD ? n * VEC + e : 0]);
+                const int f0 = VEC == 1 ? o1 : e < VEC / 2 ? o1 + 2 * e : o2 + 2 * e - VEC;
+                red[grp * p.D + f0] = f.x;
+                red[grp * p.D + (VEC == 1 ? o2 : f0 + 1)] = f.y;
             }
-            __syncthreads();
-            for (int d = tid; d < p.D; d += THREADS) {
-                float s = 0.f;
-                for (int i = 0; i < groups; ++i) s += red[i * p.D + d];
-                p.part[((size_t)blockIdx.x * 2 + sdi) * p.D + d] = s;
-            }
+        }
+        __syncthreads();
+        for (int d = tid; d < p.D; d += THREADS) {
+            float s = 0.f;
+            for (int i = 0; i < groups; ++i) s += red[i * p.D + d];
+            p.part[((size_t)blockIdx.x * 2 + blockIdx.y) * p.D + d] = s;
         }
     }
 }
 
-// dw[side][d] = sum over the CTAs' partials, 32 columns a CTA, 8 rows of it side by side.
-__global__ void __launch_bounds__(256)
+// dw[side][d] = sum over the CTAs' partials, 32 columns a CTA, 32 rows of it side by side.
+__global__ void __launch_bounds__(1024)
 weight_sum_kernel(const float *__restrict__ part, int n, int D, float *dwq, float *dwk)
 {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, sdi = blockIdx.y, d = blockIdx.x * 32 + tx;
     griddep_wait();
     griddep_launch_dependents();
     float s = 0.f;
     if (d < D)
-        for (int i = ty; i < n; i += 8) s += part[((size_t)i * 2 + sdi) * D + d];
+#pragma unroll 8
+        for (int i = ty; i < n; i += 32) s += part[((size_t)i * 2 + sdi) * D + d];
     red[ty][tx] = s;
     __syncthreads();
     float *dw = sdi ? dwk : dwq;
-    if (ty == 0 && d < D && dw) {
-        for (int i = 1; i < 8; ++i) s += red[i][tx];
-        dw[d] = s;
-    }
+    s = warp_sum(red[tx][ty]);   // column ty of the tile
+    const int col = blockIdx.x * 32 + ty;
+    if (tx == 0 && col < D && dw) dw[col] = s;
 }
 
-// CTAs of a launch: enough for every SM four times over, no more than there are tiles.
+// CTAs of a backward launch at most: every one leaves partial sums of the weights' gradients.
 constexpr int MAX_CTAS = 148 * 4;
 
 // The widest vector that divides the parts a unit is cut from and that every address is a multiple of.
@@ -280,57 +401,41 @@ int vector_width(const Params &p, int esize, bool inter, bool bwd)
         }
         return true;
     };
-    for (int vec = 16 / esize; vec > 1; vec /= 2)
+    for (int vec = 4; vec > 1; vec /= 2)
         if (fits(vec)) return vec;
     return 1;
 }
 
-template <typename T, int VEC, bool INTER, bool BWD>
-cudaError_t launch(Params p, int ctas, cudaStream_t stream)
+template <typename T, int VEC, int SPAN, bool INTER, bool BWD>
+cudaError_t launch(Params p, int *ctas, cudaStream_t stream)
 {
-    const int units = p.D / 2 / VEC;
+    const int units = p.D / 2 / VEC, heads = std::max(p.side[0].heads, p.side[1].heads);
     p.GL = 1;
     while (p.GL < 32 && p.GL < units) p.GL *= 2;
-    size_t smem = sizeof(float2) * p.TT * (p.RD / 2);
-    if (BWD && p.part) smem = std::max(smem, sizeof(float) * (THREADS / p.GL) * p.D);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = ensure_dynamic_smem((const void *)qknorm_kernel<T, VEC, INTER, BWD>, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_kernel(qknorm_kernel<T, VEC, INTER, BWD>, dim3(ctas), dim3(THREADS), smem, stream, 1, p);
+    const int groups = THREADS / p.GL;
+    // a token's heads go to as many groups as it takes to fill the GPU's threads once
+    p.HS = (int)std::min<long long>(heads, std::max<long long>(1, 148ll * 1024 / p.GL / p.tokens));
+    const unsigned long long need = ((unsigned long long)p.tokens * p.HS + groups - 1) / groups;
+    *ctas = (int)std::min<unsigned long long>(need, BWD ? MAX_CTAS : 1ull << 30);
+    const size_t smem = BWD && p.part ? sizeof(float) * groups * p.D : 0;
+    return launch_kernel(qknorm_kernel<T, VEC, SPAN, INTER, BWD>, dim3((unsigned)*ctas, 2), dim3(THREADS), smem, stream, 1, p);
 }
 
 template <typename T, int VEC, bool BWD>
-cudaError_t launch_inter(const Params &p, bool inter, int ctas, cudaStream_t stream)
+cudaError_t launch_vec(const Params &p, bool inter, int *ctas, cudaStream_t stream)
 {
-    return inter ? launch<T, VEC, true, BWD>(p, ctas, stream) : launch<T, VEC, false, BWD>(p, ctas, stream);
+    if (p.D <= 256) return inter ? launch<T, VEC, 4, true, BWD>(p, ctas, stream) : launch<T, VEC, 4, false, BWD>(p, ctas, stream);
+    return inter ? launch<T, VEC, 8, true, BWD>(p, ctas, stream) : launch<T, VEC, 8, false, BWD>(p, ctas, stream);
 }
 
-template <bool BWD>
-cudaError_t dispatch(const Params &p, bool bf16, bool inter, int ctas, cudaStream_t stream)
+template <typename T, bool BWD>
+cudaError_t dispatch(const Params &p, bool inter, int *ctas, cudaStream_t stream)
 {
-    const int vec = vector_width(p, bf16 ? 2 : 4, inter, BWD);
-    if (bf16) {
-        switch (vec) {
-        case 8: return launch_inter<__nv_bfloat16, 8, BWD>(p, inter, ctas, stream);
-        case 4: return launch_inter<__nv_bfloat16, 4, BWD>(p, inter, ctas, stream);
-        case 2: return launch_inter<__nv_bfloat16, 2, BWD>(p, inter, ctas, stream);
-        default: return launch_inter<__nv_bfloat16, 1, BWD>(p, inter, ctas, stream);
-        }
+    switch (vector_width(p, (int)sizeof(T), inter, BWD)) {
+    case 4: return launch_vec<T, 4, BWD>(p, inter, ctas, stream);
+    case 2: return launch_vec<T, 2, BWD>(p, inter, ctas, stream);
+    default: return launch_vec<T, 1, BWD>(p, inter, ctas, stream);
     }
-    switch (vec) {
-    case 4: return launch_inter<float, 4, BWD>(p, inter, ctas, stream);
-    case 2: return launch_inter<float, 2, BWD>(p, inter, ctas, stream);
-    default: return launch_inter<float, 1, BWD>(p, inter, ctas, stream);
-    }
-}
-
-// Tokens per tile: one while there are few (a decode step spreads over the GPU), else four.
-int tile_tokens(long long tokens) { return tokens <= 2 * MAX_CTAS ? 1 : 4; }
-int cta_count(long long tokens)
-{
-    const int tt = tile_tokens(tokens);
-    return (int)std::min<long long>((tokens + tt - 1) / tt, MAX_CTAS);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -341,7 +446,8 @@ mlstm_status check(const Params &p, mlstm_dtype dt, int NHQ, int NHK, qknorm_kin
     if (kind != QKNORM_RMS && kind != QKNORM_L2) return MLSTM_ERR_INVALID_ARG;
     if (!(p.eps >= 0.f)) return MLSTM_ERR_INVALID_ARG;
     if (dt != MLSTM_F32 && dt != MLSTM_BF16) return MLSTM_ERR_UNSUPPORTED;
-    if (p.D < 8 || p.D > 512 || p.D % 8 || NHQ > 65535 || NHK > 65535) return MLSTM_ERR_UNSUPPORTED;
+    if (p.D < 8 || p.D > 512 || p.D % 8 || NHQ > 4096 || NHK > 4096) return MLSTM_ERR_UNSUPPORTED;
+    if ((long long)p.B * p.S > (1ll << 31) - 1) return MLSTM_ERR_UNSUPPORTED;
     if (p.tokens == 0 || NHQ + NHK == 0) return MLSTM_OK;
     const uintptr_t es = dt == MLSTM_BF16 ? 2 : 4;
     for (const Side &sd : p.side) {
@@ -367,10 +473,9 @@ Params make_params(const float *inv_freq, const int *positions, int B, int S, in
     Params p = {};
     p.inv_freq = inv_freq;
     p.positions = positions;
-    p.tokens = B > 0 && S > 0 ? (long long)B * S : 0;
+    p.tokens = B > 0 && S > 0 ? (unsigned)((long long)B * S) : 0u;
     p.B = B; p.S = S; p.D = D; p.RD = RD;
     p.l2 = kind == QKNORM_L2;
-    p.TT = tile_tokens(p.tokens);
     p.eps = eps;
     return p;
 }
@@ -395,15 +500,17 @@ mlstm_status qknorm_fwd(const void *q, qknorm_strides q_strides, const void *k, 
     p.side[1] = make_side(k, k_strides, nullptr, k_out, none, k_weight, NHK);
     const mlstm_status st = check(p, dt, NHQ, NHK, kind, false);
     if (st != MLSTM_OK || p.tokens == 0 || NHQ + NHK == 0) return st;
-    const cudaError_t e = dispatch<false>(p, dt == MLSTM_BF16, interleaved != 0, cta_count(p.tokens),
-                                          static_cast<cudaStream_t>(stream));
+    int ctas = 0;
+    const cudaError_t e = dt == MLSTM_BF16
+        ? dispatch<__nv_bfloat16, false>(p, interleaved != 0, &ctas, static_cast<cudaStream_t>(stream))
+        : dispatch<float, false>(p, interleaved != 0, &ctas, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLSTM_OK : MLSTM_ERR_CUDA;
 }
 
 size_t qknorm_bwd_workspace_size(int B, int S, int NHQ, int NHK, int D)
 {
     if (B <= 0 || S <= 0 || NHQ < 0 || NHK < 0 || D < 8 || D > 512 || D % 8) return 0;
-    return sizeof(float) * 2 * D * (size_t)cta_count((long long)B * S);
+    return sizeof(float) * 2 * D * (size_t)MAX_CTAS;
 }
 
 mlstm_status qknorm_bwd(const void *d_q_out, const void *d_k_out, const void *q, qknorm_strides q_strides,
@@ -426,15 +533,16 @@ mlstm_status qknorm_bwd(const void *d_q_out, const void *d_k_out, const void *q,
         if (dk_weight && e == cudaSuccess) e = cudaMemsetAsync(dk_weight, 0, sizeof(float) * D, s);
         return e == cudaSuccess ? MLSTM_OK : MLSTM_ERR_CUDA;
     }
-    const int ctas = cta_count(p.tokens);
+    int ctas = 0;
     if (dq_weight || dk_weight) {
-        if (!workspace || workspace_bytes < sizeof(float) * 2 * D * (size_t)ctas) return MLSTM_ERR_WORKSPACE;
+        if (!workspace || workspace_bytes < sizeof(float) * 2 * D * (size_t)MAX_CTAS) return MLSTM_ERR_WORKSPACE;
         if (!aligned(workspace, 16)) return MLSTM_ERR_INVALID_ARG;
         p.part = static_cast<float *>(workspace);
     }
-    cudaError_t e = dispatch<true>(p, dt == MLSTM_BF16, interleaved != 0, ctas, s);
+    cudaError_t e = dt == MLSTM_BF16 ? dispatch<__nv_bfloat16, true>(p, interleaved != 0, &ctas, s)
+                                     : dispatch<float, true>(p, interleaved != 0, &ctas, s);
     if (e == cudaSuccess && p.part)
-        e = launch_kernel(weight_sum_kernel, dim3((D + 31) / 32, 2), dim3(256), 0, s, 1, p.part, ctas, D, dq_weight,
+        e = launch_kernel(weight_sum_kernel, dim3((D + 31) / 32, 2), dim3(1024), 0, s, 1, p.part, ctas, D, dq_weight,
                           dk_weight);
     return e == cudaSuccess ? MLSTM_OK : MLSTM_ERR_CUDA;
 }

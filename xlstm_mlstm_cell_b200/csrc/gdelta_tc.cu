@@ -228,10 +228,13 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
             if (warp == 0) {
                 float2 a0, a1;
-                if (w.A) chunk_gates(g + gt, len, lane, 1.0, w.A[ch * 64 + 2 * lane], w.A[ch * 64 + 2 * lane + 1]);
                 const float b0 = 2 * lane < len ? beta[gt + 2 * lane] : 0.f;
                 const float b1 = 2 * lane + 1 < len ? beta[gt + 2 * lane + 1] : 0.f;
                 chunk_gates_log2(g + gt, len, lane, a0, a1);
+                if (w.A) {
+                    w.A[ch * 64 + 2 * lane] = a0;
+                    w.A[ch * 64 + 2 * lane + 1] = a1;
+                }
                 ga[2 * lane] = make_float4(a0.x, a0.y, b0, 0.f);
                 ga[2 * lane + 1] = make_float4(a1.x, a1.y, b1, 0.f);
             }

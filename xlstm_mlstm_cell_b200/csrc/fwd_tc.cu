@@ -1234,6 +1234,20 @@ bool make_map(CUtensorMap *m, const void *base, int D, int S, int BH, int rows)
     return r == CUDA_SUCCESS;
 }
 
+bool make_map_f32(CUtensorMap *m, const void *base, int C, int R, int Z)
+{
+    auto enc = get_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)C, (cuuint64_t)R, (cuuint64_t)Z};
+    cuuint64_t strides[2] = {(cuuint64_t)C * 4, (cuuint64_t)R * C * 4};
+    cuuint32_t box[3] = {16, 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 template <int DK, int L>
 cudaError_t launch_dk_l(const FwdArgs &a, const FwdWorkspace &w, const PhaseMark &mark)
 {

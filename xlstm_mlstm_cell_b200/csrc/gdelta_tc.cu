@@ -378,10 +378,16 @@ struct Walk {
     static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
     static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : 64;   // (reverse: K's tokens, then Q's)
     static constexpr uint32_t DO = YN + NCH * BLOCKS * YROWS * 128; // reverse: dO, 64 rows, the chains side by side
-    static constexpr uint32_t BAR = DO + (MODE == REVERSE ? 8192 : 0);
+    // the backward: an epilogue warp's 32 rows of fp32 results on their way out, 2 KB each: states of every warp,
+    // tokens' rows of the K tokens' warps
+    static constexpr uint32_t OS = DO + (MODE == REVERSE ? 8192 : 0), OT = OS + (MODE == FORWARD ? 0 : NCH * EPI * 2048);
+    static constexpr uint32_t BAR = OT + (MODE == FORWARD ? 0 : NCH * EPI * 1024);
     static constexpr uint32_t NBAR = 2 * STAGES + 7 * NCH;
     static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
-    static constexpr uint32_t TMEM_COLS = CW == 32 ? 512 : 256;   // per chain X and then D, [E; F]: 3 CW each
+    // TMEM columns of a chain: X and [E; F], 3 CW each; D over X, or (reverse) beside them with G^T dO
+    static constexpr uint32_t TX = 0, TE = 3 * CW, TD = MODE == REVERSE ? 6 * CW : 0, TG = 9 * CW;
+    static constexpr uint32_t TCH = MODE == REVERSE ? 10 * CW : 6 * CW;
+    static constexpr uint32_t TMEM_COLS = NCH * TCH > 256 ? 512 : 256;
 };
 
 struct WalkParams {
@@ -397,7 +403,8 @@ struct WalkParams {
 
 template <int CW, int KS, int MODE>
 __global__ void __launch_bounds__(Walk<CW, MODE>::THREADS, 1)
-walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const WalkParams p)
+walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_t, const WalkParams p)
 {
     using W = Walk<CW, MODE>;
     static_assert(MODE != REVERSE || CW == 16, "dO of both chains in one block of columns");
@@ -422,7 +429,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&x_done[h], 1);
             mbar_init(&y_ready[h], W::EPI / 2);
             mbar_init(&e_done[h], 1);
-            mbar_init(&n_ready[h], W::EPI);
+            mbar_init(&n_ready[h], MODE == REVERSE ? W::EPI / 2 : W::EPI);
             mbar_init(&d_done[h], 1);
             mbar_init(&o_ready[h], W::EPI / 2);
         }
@@ -430,6 +437,10 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         fence_barrier_init();
         tma_prefetch(&tm_q);
         tma_prefetch(&tm_k);
+        if (MODE != FORWARD) {
+            tma_prefetch(&tm_s);
+            tma_prefetch(&tm_t);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, W::TMEM_COLS);
@@ -439,7 +450,9 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    griddep_wait();
+    // The reverse walk reads nothing of the forward recomputation launched just before it, only what that one
+    // waited for; so it runs beside its last CTAs and waits for it at its own end, for the kernel behind
+    if (MODE != REVERSE) griddep_wait();
     griddep_launch_dependents();
     const int n = live_tokens(p.lengths, b, p.S), nc = (n + CH - 1) / CH;
 
@@ -465,7 +478,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             constexpr uint32_t IDD = idesc_bf16(128, 3 * CW, 1, 1);
             constexpr uint32_t BS = W::BLOCKS * 1024, BY = W::BLOCKS * W::YROWS * 8;   // a chain's operands, 16-byte units
             // reverse: T^T and G^T, M = 64; the 64 M behind read what lies behind, into lanes that nothing uses
-            constexpr uint32_t IDT = idesc_bf16(128, 3 * CW, 1, 1), IDTM = idesc_bf16(128, 2 * CW, 1, 1), IDG = idesc_bf16(128, CW, 1, 1);
+            constexpr uint32_t IDTM = idesc_bf16(128, 2 * CW, 1, 1), IDG = idesc_bf16(128, CW, 1, 1);
             const uint64_t atm = smem_desc(smem_u32(smem) + 32768, 8192, 1024);
             const uint64_t bo = MODE == REVERSE ? smem_desc(smem_u32(smem + W::DO), 8192, 1024) : 0;
             const uint64_t bs = smem_desc(smem_u32(smem + W::SP), 16384, 1024);
@@ -478,57 +491,59 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const uint64_t so = (uint64_t)st * (W::STAGE / 16);
                 const uint32_t ph = (uint32_t)c & 1u;
                 ok = mbar_wait(&full[st], (uint32_t)(c / NST) & 1u, wc);
-#pragma unroll
-                for (int h = 0; h < NCH && ok; ++h) {
-                    if (!(ok = mbar_wait(&s_ready[h], ph, wc))) break;
+                auto issue_x = [&](int h) {
+                    if (!(ok = ok && mbar_wait(&s_ready[h], ph, wc))) return;
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < KS; ++k)
-                        mma_ss(tmem + h * 6 * CW, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+                        mma_ss(tmem + h * W::TCH + W::TX, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
                                bs + (uint64_t)(h * BS + k * 128), IDX, k > 0);
                     mma_commit(&x_done[h]);
-                    if (MODE == REVERSE) {
-                        if (!(ok = mbar_wait(&o_ready[h], ph, wc))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)   // G's rows lie 8 KB into the values' tile, and 16 KB further its residues'
-                            mma_ss(tmem + h * 6 * CW + 3 * CW, atm + so + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
-                                   bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, k > 0);
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < NCH && ok; ++h) {
-                    if (!(ok = mbar_wait(&y_ready[h], ph, wc))) break;
+                };
+                // reverse: G^T dO, and the update's share of Q's tokens; neither waits for the state
+                auto issue_q = [&](int h) {
+                    if (!(ok = ok && mbar_wait(&o_ready[h], ph, wc))) return;
                     tc_fence_after();
-                    const uint32_t de = tmem + h * 6 * CW + 3 * CW;
-                    if (MODE != REVERSE) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ss(de, at + so + (uint64_t)(k * 2), by + (uint64_t)(h * BY + k * 128), IDX, k > 0);
+                    for (int k = 7; k >= 0; --k)   // G's rows lie 8 KB into the values' tile, and 16 KB further its residues'
+                        mma_ss(tmem + h * W::TCH + W::TG, atm + so + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
+                               bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, k < 7);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
-                            mma_ss(de, at + so + (uint64_t)(1024 + k * 2), by + (uint64_t)(h * BY + k * 128), IDM, 1);
-                    } else {
+                    for (int k = 4; k < 8; ++k)
+                        mma_ss(tmem + h * W::TCH + W::TD, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 4);
+                };
+                auto issue_e = [&](int h) {
+                    if (!(ok = ok && mbar_wait(&y_ready[h], ph, wc))) return;
+                    tc_fence_after();
+                    const uint32_t de = tmem + h * W::TCH + W::TE;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {   // the first part's columns onto G^T dO, the others from zero
-                            mma_ss(de, atm + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDG, 1);
-                            mma_ss(de + CW, atm + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128 + CW / 8), IDTM, k > 0);
-                        }
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(de, MODE == REVERSE ? atm + so + (uint64_t)(k * 128) : at + so + (uint64_t)(k * 2),
+                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDD : IDX, k > 0);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ss(de, atm + so + (uint64_t)(1024 + k * 128), by + (uint64_t)(h * BY + k * 128), IDTM, 1);
-                    }
+                    for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
+                        mma_ss(de, MODE == REVERSE ? atm + so + (uint64_t)(1024 + k * 128) : at + so + (uint64_t)(1024 + k * 2),
+                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDTM : IDM, 1);
                     mma_commit(&e_done[h]);
-                }
-#pragma unroll
-                for (int h = 0; h < NCH && ok; ++h) {
-                    if (!(ok = mbar_wait(&n_ready[h], ph, wc))) break;
+                };
+                auto issue_d = [&](int h) {
+                    if (!(ok = ok && mbar_wait(&n_ready[h], ph, wc))) return;
                     tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < (int)W::YROWS / 16; ++k)   // over X, which every warp has read
-                        mma_ss(tmem + h * 6 * CW, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 0);
+                    for (int k = 0; k < 4; ++k)   // forward: over X, which every warp has read
+                        mma_ss(tmem + h * W::TCH + W::TD, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD,
+                               MODE == REVERSE || k > 0);
                     mma_commit(&d_done[h]);
+                };
+#pragma unroll
+                for (int h = 0; h < NCH; ++h) issue_x(h);
+#pragma unroll
+                for (int h = 0; h < NCH; ++h) {
+                    if (MODE == REVERSE) issue_q(h);
+                    issue_e(h);
                 }
+#pragma unroll
+                for (int h = 0; h < NCH; ++h) issue_d(h);
                 if (ok) mma_commit(&empty[st]);
             }
         }
@@ -537,7 +552,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const int row = quad * 32 + lane, t = row & 63;        // TMEM lane; token of the chunk
         const bool krow = quad < 2;
         const int col = blockIdx.x * W::VT + h * CW + cg * 16; // first of the thread's 16 value columns
-        const uint32_t tl = tmem_addr(tmem, quad * 32, h * 6 * CW + cg * 16);
+        const uint32_t tl = tmem_addr(tmem, quad * 32, h * W::TCH + cg * 16);
         uint8_t *sp = smem + W::SP + h * W::BLOCKS * 16384, *yn = smem + W::YN + h * W::BLOCKS * W::YROWS * 128;
         uint64_t s[8];                                         // row `row` of the state, in pairs
         const size_t srow = ((size_t)bhv * p.DK + row) * p.DV + col;
@@ -549,6 +564,21 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             s[2 * e] = f2_pack(x.x, x.y);
             s[2 * e + 1] = f2_pack(x.z, x.w);
         }
+        // the warp's 32 rows of 16 fp32 columns to rows r0 .. of chunk ci's array, by way of `buf`
+        auto send = [&](uint8_t *buf, const CUtensorMap &tm, int r0, int ci, const uint64_t (&x)[8]) {
+            if (live_cols <= 0) return;
+            if (lane == 0) bulk_wait_read0();
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<ulonglong2 *>(buf + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) = make_ulonglong2(x[2 * e], x[2 * e + 1]);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_3d(&tm, buf, col, r0, bhv * p.w.NC + ci);
+                bulk_commit();
+            }
+        };
         for (int c = 0; c < nc; ++c) {
             const uint32_t ph = (uint32_t)c & 1u;
             const int ci = MODE == REVERSE ? nc - 1 - c : c, len = min(CH, n - ci * CH);
@@ -557,12 +587,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_ready[h]);
-            if (MODE != FORWARD && row < p.DK) {
-                float *keep = (MODE == KEEP ? p.w.SC : p.w.DSC) + (((size_t)bhv * p.w.NC + ci) * p.DK + row) * p.DV + col;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (4 * e < live_cols) *reinterpret_cast<ulonglong2 *>(keep + 4 * e) = make_ulonglong2(s[2 * e], s[2 * e + 1]);
-            }
+            if (MODE != FORWARD && quad * 32 < p.DK) send(smem + W::OS + (warp - 2) * 2048, tm_s, quad * 32, ci, s);
             // the token's gates and its row of V (reverse: dO, the rows of Q's warps): asked for here, they
             // arrive while X is computed; a load in flight at one of the fences would hold it up.  The next
             // chunk's row is brought to L2
@@ -584,13 +609,22 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (MODE == REVERSE && !krow) {   // dO itself, and scale e^a dO behind the K tokens' rows
 #pragma unroll
                 for (int e = 0; e < 2; ++e) *reinterpret_cast<uint4 *>(smem + W::DO + sw128_chunk(t, h * (CW / 8) + cg * 2 + e, 64)) = vr[e];
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&o_ready[h]);
                 const uint64_t f = f2_pack(p.scale * ea, p.scale * ea);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = f2_mul(f, f2_from_bf16x2((&vr[e >> 2].x)[e & 3]));
                 store_parts(yn, row, cg * 2, CW / 8, W::YROWS, x);
+                if (len < CH) {   // padding, as for K below; the tile has to have landed
+                    if (!mbar_wait(&full[c % NST], (uint32_t)(c / NST) & 1u, wc)) break;
+                    if (h == 0 && cg == 0 && t >= len) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            *reinterpret_cast<uint4 *>(smem + (c % NST) * W::STAGE + sw128_chunk(64 + t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_ready[h]);
             }
             if (!mbar_wait(&x_done[h], ph, wc)) break;
             tc_fence_after();
@@ -611,22 +645,23 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&y_ready[h]);
-            } else {
-                if (MODE == REVERSE) {
-                    if (h == 0 && cg == 0 && t >= len) {   // as for K below
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(64 + t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async();
-                }
+            } else if (MODE != REVERSE) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&n_ready[h]);   // X is read (reverse: and Q's rows written)
+                if (lane == 0) mbar_arrive(&n_ready[h]);   // X is read
             }
             if (!mbar_wait(&e_done[h], ph, wc)) break;
             tc_fence_after();
-            if (krow || MODE == FORWARD) load_parts(tl + 3 * CW, CW, y);
+            if (krow || MODE == FORWARD) load_parts(tl + W::TE, CW, y);
             if (krow) {
+                if (MODE == REVERSE) {
+                    uint32_t go[16];
+                    tmem_ld16(tl + W::TG, go);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        y[e] = f2_add(y[e], f2_pack(__uint_as_float(go[2 * e]), __uint_as_float(go[2 * e + 1])));
+                }
                 const float fn = MODE == REVERSE ? -ea : eo;
                 const uint64_t f = f2_pack(fn, fn);
 #pragma unroll
@@ -645,12 +680,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&n_ready[h]);
-                if (MODE != FORWARD) {
-                    float *keep = (MODE == KEEP ? p.w.E : p.w.DV) + (((size_t)bhv * p.w.NC + ci) * 64 + t) * p.DV + col;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * e < live_cols) *reinterpret_cast<ulonglong2 *>(keep + 4 * e) = make_ulonglong2(x[2 * e], x[2 * e + 1]);
-                }
+                if (MODE != FORWARD) send(smem + W::OT + (h * W::EPI / 2 + cg * 2 + quad) * 2048, tm_t, quad * 32, ci, x);
             }
             if (MODE == FORWARD ? !krow && t < len : MODE == REVERSE && krow && t < len) {
                 __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + ci * CH + t) * p.DV + col;
@@ -667,11 +697,12 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if (!mbar_wait(&d_done[h], ph, wc)) break;
             tc_fence_after();
-            load_parts(tl, CW, y);
+            load_parts(tl + W::TD, CW, y);
             const uint64_t f = f2_pack(ef, ef);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = f2_fma(f, s[e], y[e]);
         }
+        if (MODE != FORWARD && lane == 0) bulk_wait0();   // the warp's results are on their way no longer
         if (MODE != KEEP && p.S_final && row < p.DK) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -697,11 +728,12 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         tc_fence_after();
         tmem_dealloc(tmem, W::TMEM_COLS);
     }
+    if (MODE == REVERSE) griddep_wait();
 }
 
 template <int CW, int KS, int MODE>
-cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap &mq, const CUtensorMap &mk, const void *v,
-                           const float *S0, void *o, float *S_final)
+cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap (&m)[4], const void *v, const float *S0,
+                           void *o, float *S_final)
 {
     using W = Walk<CW, MODE>;
     cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<CW, KS, MODE>, W::TOTAL);
@@ -709,22 +741,28 @@ cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap 
     WalkParams p = {static_cast<const __nv_bfloat16 *>(v), S0, a.lengths, static_cast<__nv_bfloat16 *>(o), S_final, a.NH,
                     a.NHV, a.S, a.DK, a.DV, a.scale, w};
     return launch_kernel(walk_tc_kernel<CW, KS, MODE>, dim3((a.DV + W::VT - 1) / W::VT, a.B * a.NHV), dim3(W::THREADS),
-                         W::TOTAL, a.stream, 1, mq, mk, p);
+                         W::TOTAL, a.stream, 1, m[0], m[1], m[2], m[3], p);
 }
 
 template <int MODE>
 cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const void *v, const float *S0, void *o, float *S_final)
 {
-    CUtensorMap mq, mk;
-    if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
+    CUtensorMap m[4];   // q, k, and where the states' and the tokens' results go
+    if (!tcfwd::make_map(&m[0], a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&m[1], a.k, a.DK, a.S, a.B * a.NH, CH))
         return cudaErrorUnknown;
-    // a chunk takes longer the more columns a CTA has, so the columns are split while the GPU has SMs for it
-    const bool narrow = MODE == REVERSE || (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
-    if constexpr (MODE != REVERSE)
-        if (!narrow) return a.DK > 64 ? launch_walk_cw<32, 8, MODE>(a, w, mq, mk, v, S0, o, S_final)
-                                      : launch_walk_cw<32, 4, MODE>(a, w, mq, mk, v, S0, o, S_final);
-    return a.DK > 64 ? launch_walk_cw<16, 8, MODE>(a, w, mq, mk, v, S0, o, S_final)
-                     : launch_walk_cw<16, 4, MODE>(a, w, mq, mk, v, S0, o, S_final);
+    m[2] = m[3] = m[0];
+    if (MODE != FORWARD && (!tcfwd::make_map_f32(&m[2], MODE == KEEP ? w.SC : w.DSC, a.DV, a.DK, a.B * a.NHV * w.NC) ||
+                            !tcfwd::make_map_f32(&m[3], MODE == KEEP ? w.E : w.DV, a.DV, 64, a.B * a.NHV * w.NC)))
+        return cudaErrorUnknown;
+    // While the GPU has SMs for it a CTA takes 32 columns; 64 take fewer CTAs than twice the time (the epilogue
+    // warps of the K tokens, two of the SM's four schedulers, are what a chunk then waits for).  The backward's
+    // walks always take 32: their results' way out takes the shared memory
+    const bool narrow = MODE != FORWARD || (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
+    if constexpr (MODE == FORWARD)
+        if (!narrow) return a.DK > 64 ? launch_walk_cw<32, 8, MODE>(a, w, m, v, S0, o, S_final)
+                                      : launch_walk_cw<32, 4, MODE>(a, w, m, v, S0, o, S_final);
+    return a.DK > 64 ? launch_walk_cw<16, 8, MODE>(a, w, m, v, S0, o, S_final)
+                     : launch_walk_cw<16, 4, MODE>(a, w, m, v, S0, o, S_final);
 }
 
 }  // namespace

@@ -21,6 +21,10 @@ struct Params {
 // [BH][S][D] bf16 tensor map with boxes of 64 columns x `rows` tokens x 1 head, 128-byte swizzle.
 bool make_map(CUtensorMap *m, const void *base, int D, int S, int BH, int rows);
 
+// [Z][R][C] fp32 tensor map with boxes of 16 columns x 32 rows x 1, 64-byte swizzle (a warp's share of a tile
+// on its way out).
+bool make_map_f32(CUtensorMap *m, const void *base, int C, int R, int Z);
+
 // The walk over CTA pairs (walk_pair.cu): taken for these head sizes and chunk length.
 bool walk_pair_supported(int DK, int DV, int L);
 // Launches it; q, k, v the bf16 inputs [BH][S][DK | DV].

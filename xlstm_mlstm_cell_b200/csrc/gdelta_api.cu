@@ -127,8 +127,16 @@ mlstm_status gdelta_fwd(const void *q, const void *k, const void *v, const float
             e = launch_state_copy(S0, S_final, (size_t)B * NHV * DK * DV, a.stream);
         return cuda_status(e);
     }
-    cudaError_t e = w.TG ? launch_prep_tc(a, w) : launch_prep(a, w, false);
-    if (e == cudaSuccess) e = w.TG ? launch_forward_tc(a, w, o, S_final) : launch_walk(a, w, o, S_final, false);
+    cudaError_t e;
+    if (w.TG) {
+        Maps m;
+        if (!make_maps(a, &m)) return MLSTM_ERR_CUDA;
+        e = launch_prep_tc(a, w, m);
+        if (e == cudaSuccess) e = launch_forward_tc(a, w, m, o, S_final);
+    } else {
+        e = launch_prep(a, w, false);
+        if (e == cudaSuccess) e = launch_walk(a, w, o, S_final, false);
+    }
     return cuda_status(e);
 }
 
@@ -173,12 +181,20 @@ mlstm_status gdelta_bwd(const void *q, const void *k, const void *v, const float
             e = launch_state_copy(dS_final, dS0, (size_t)B * NHV * DK * DV, a.stream);
         return cuda_status(e);
     }
-    cudaError_t e = w.TG ? launch_prep_tc(a, w) : launch_prep(a, w, true);
-    if (e == cudaSuccess) e = w.TG ? launch_keep_tc(a, w) : launch_walk(a, w, nullptr, nullptr, true);
-    if (e == cudaSuccess)
-        e = w.TG ? launch_reverse_tc(a, w, d_o, dS_final, dv, dS0) : launch_reverse(a, w, d_o, dS_final, dv, dS0);
-    if (e == cudaSuccess)
-        e = w.TG ? launch_grad_tc(a, w, d_o, dq, dk, dg, dbeta) : launch_grad(a, w, d_o, dq, dk, dg, dbeta);
+    cudaError_t e;
+    if (w.TG) {
+        Maps m;
+        if (!make_maps(a, &m)) return MLSTM_ERR_CUDA;
+        e = launch_prep_tc(a, w, m);
+        if (e == cudaSuccess) e = launch_keep_tc(a, w, m);
+        if (e == cudaSuccess) e = launch_reverse_tc(a, w, m, d_o, dS_final, dv, dS0);
+        if (e == cudaSuccess) e = launch_grad_tc(a, w, m, d_o, dq, dk, dg, dbeta);
+    } else {
+        e = launch_prep(a, w, true);
+        if (e == cudaSuccess) e = launch_walk(a, w, nullptr, nullptr, true);
+        if (e == cudaSuccess) e = launch_reverse(a, w, d_o, dS_final, dv, dS0);
+        if (e == cudaSuccess) e = launch_grad(a, w, d_o, dq, dk, dg, dbeta);
+    }
     return cuda_status(e);
 }
 

@@ -558,12 +558,9 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
 }  // namespace
 
-cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
-                           float *dbeta)
+cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const Maps &m, const void *d_o, void *dq, void *dk,
+                           float *dg, float *dbeta)
 {
-    CUtensorMap mq, mk;
-    if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
-        return cudaErrorUnknown;
     cudaError_t e = ensure_dynamic_smem((const void *)grad_tc_kernel, TOTAL);
     if (e != cudaSuccess) return e;
     Params p = {static_cast<const __nv_bfloat16 *>(d_o), a.beta, a.lengths, static_cast<__nv_bfloat16 *>(dq),
@@ -572,7 +569,7 @@ cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const void *d_o, v
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
     const long long items = (long long)w.NC * a.B * a.NH;
     return launch_kernel(grad_tc_kernel, dim3((unsigned)std::min<long long>(items, sms)), dim3(THREADS), TOTAL, a.stream, 1,
-                         mq, mk, p);
+                         m.q, m.k, p);
 }
 
 }  // namespace gdelta

@@ -1,6 +1,7 @@
 // gdelta_internal.h -- launch descriptors of the gated delta rule's kernels.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
@@ -47,15 +48,18 @@ cudaError_t launch_reverse(const Args &a, const Workspace &w, const void *d_o, c
 // dq, dk, dg, dbeta of every chunk from the workspace.
 cudaError_t launch_grad(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
                         float *dbeta);
-// The same on the tensor cores, for the shapes that tc_supported names (workspace: GB, TG).
+// The same on the tensor cores, for the shapes that tc_supported names (workspace: GB, TG).  The kernels
+// of one call share the tensor maps of q and k.
+struct Maps { CUtensorMap q, k; };
 bool tc_supported(bool bf16, int DK, int DV);
-cudaError_t launch_prep_tc(const Args &a, const Workspace &w);
-cudaError_t launch_forward_tc(const Args &a, const Workspace &w, void *o, float *S_final);
-cudaError_t launch_keep_tc(const Args &a, const Workspace &w);
-cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv,
-                              float *dS0);
-cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const void *d_o, void *dq, void *dk, float *dg,
-                           float *dbeta);
+bool make_maps(const Args &a, Maps *m);
+cudaError_t launch_prep_tc(const Args &a, const Workspace &w, const Maps &m);
+cudaError_t launch_forward_tc(const Args &a, const Workspace &w, const Maps &m, void *o, float *S_final);
+cudaError_t launch_keep_tc(const Args &a, const Workspace &w, const Maps &m);
+cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const Maps &m, const void *d_o, const float *dS_final,
+                              void *dv, float *dS0);
+cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const Maps &m, const void *d_o, void *dq, void *dk,
+                           float *dg, float *dbeta);
 cudaError_t launch_state_copy(const float *S0, float *S_final, size_t n, cudaStream_t stream);
 
 struct StepArgs {

@@ -745,12 +745,10 @@ cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap 
 }
 
 template <int MODE>
-cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const void *v, const float *S0, void *o, float *S_final)
+cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const Maps &qk, const void *v, const float *S0, void *o,
+                           float *S_final)
 {
-    CUtensorMap m[4];   // q, k, and where the states' and the tokens' results go
-    if (!tcfwd::make_map(&m[0], a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&m[1], a.k, a.DK, a.S, a.B * a.NH, CH))
-        return cudaErrorUnknown;
-    m[2] = m[3] = m[0];
+    CUtensorMap m[4] = {qk.q, qk.k, qk.q, qk.q};   // q, k, and where the states' and the tokens' results go
     if (MODE != FORWARD && (!tcfwd::make_map_f32(&m[2], MODE == KEEP ? w.SC : w.DSC, a.DV, a.DK, a.B * a.NHV * w.NC) ||
                             !tcfwd::make_map_f32(&m[3], MODE == KEEP ? w.E : w.DV, a.DV, 64, a.B * a.NHV * w.NC)))
         return cudaErrorUnknown;
@@ -769,31 +767,33 @@ cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const void *v, con
 
 bool tc_supported(bool bf16, int DK, int DV) { return bf16 && DK >= 64 && DV >= 32; }
 
-cudaError_t launch_prep_tc(const Args &a, const Workspace &w)
+bool make_maps(const Args &a, Maps *m)
 {
-    CUtensorMap mq, mk;
-    if (!tcfwd::make_map(&mq, a.q, a.DK, a.S, a.B * a.NH, CH) || !tcfwd::make_map(&mk, a.k, a.DK, a.S, a.B * a.NH, CH))
-        return cudaErrorUnknown;
+    return tcfwd::make_map(&m->q, a.q, a.DK, a.S, a.B * a.NH, CH) && tcfwd::make_map(&m->k, a.k, a.DK, a.S, a.B * a.NH, CH);
+}
+
+cudaError_t launch_prep_tc(const Args &a, const Workspace &w, const Maps &m)
+{
     const cudaError_t e = ensure_dynamic_smem((const void *)prep_tc_kernel, prep::TOTAL);
     if (e != cudaSuccess) return e;
-    return launch_kernel(prep_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, mq, mk, a.g,
-                         a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.scale, w);
+    return launch_kernel(prep_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, m.q, m.k,
+                         a.g, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.scale, w);
 }
 
-cudaError_t launch_forward_tc(const Args &a, const Workspace &w, void *o, float *S_final)
+cudaError_t launch_forward_tc(const Args &a, const Workspace &w, const Maps &m, void *o, float *S_final)
 {
-    return launch_walk_tc<FORWARD>(a, w, a.v, a.S0, o, S_final);
+    return launch_walk_tc<FORWARD>(a, w, m, a.v, a.S0, o, S_final);
 }
 
-cudaError_t launch_keep_tc(const Args &a, const Workspace &w)
+cudaError_t launch_keep_tc(const Args &a, const Workspace &w, const Maps &m)
 {
-    return launch_walk_tc<KEEP>(a, w, a.v, a.S0, nullptr, nullptr);
+    return launch_walk_tc<KEEP>(a, w, m, a.v, a.S0, nullptr, nullptr);
 }
 
-cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv,
-                              float *dS0)
+cudaError_t launch_reverse_tc(const Args &a, const Workspace &w, const Maps &m, const void *d_o, const float *dS_final,
+                              void *dv, float *dS0)
 {
-    return launch_walk_tc<REVERSE>(a, w, d_o, dS_final, dv, dS0);
+    return launch_walk_tc<REVERSE>(a, w, m, d_o, dS_final, dv, dS0);
 }
 
 }  // namespace gdelta

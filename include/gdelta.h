@@ -24,8 +24,9 @@
  *   q, k [B][NH][S][DK]; v, o [B][NHV][S][DV]  in the element type `dt`;
  *   g, beta [B][NHV][S] float32; states [B][NHV][DK][DV] float32.
  * NHV is a multiple of NH: value head h reads query and key head h / (NHV / NH).
- * Supported: DK a multiple of 8 in [8, 128], DV a multiple of 8 in [8, 512],
- * B * NHV <= 65535.
+ * Supported: DK a multiple of 8 in [8, 128], DV a multiple of 8 in [8, 512]; over
+ * sequences B * NHV <= 65535, S <= 2^30 and B * NHV * (S / 64 + 1) < 2^31, for
+ * gdelta_step B * NHV * DV / 8 < 2^31.
  * The recurrence is stable for keys of norm at most about one with beta in [0, 2];
  * nothing here normalizes them (qknorm.h does).
  *
@@ -48,10 +49,9 @@ extern "C" {
 
 /*
  * Bytes of device workspace gdelta_fwd needs (0 when the arguments are unsupported):
- * a status word, per token of a whole chunk and value head the cumulative log gates
- * (8 bytes) and per chunk and value head the two 64 x 64 matrices T and the scores in
- * fp32 (32 KB), or on the tensor-core path T and the scores' product with it as bf16
- * parts (32 KB).
+ * a status word, 8 bytes of gates per token of a whole chunk and value head, and per
+ * chunk and value head the two 64 x 64 matrices T and the scores in fp32 (32 KB), or
+ * on the tensor-core path T and the scores' product with it as bf16 parts (32 KB).
  */
 size_t gdelta_fwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, mlstm_dtype dt);
 
@@ -81,7 +81,8 @@ int gdelta_fwd_tensor_path(int DK, int DV, mlstm_dtype dt);
 
 /*
  * One token for every (b, h): updates the state IN PLACE and writes o [B][NHV][DV].
- * q, k [B][NH][DK], v [B][NHV][DV] in `dt`; g, beta [B][NHV] float32.
+ * q, k [B][NH][DK], v [B][NHV][DV] in `dt`; g, beta [B][NHV] float32 (4-byte aligned
+ * is enough for these two).
  */
 mlstm_status gdelta_step(float *state, const void *q, const void *k, const void *v, const float *g,
                          const float *beta, mlstm_dtype dt, int B, int NH, int NHV, int DK, int DV, float scale,
@@ -101,9 +102,11 @@ mlstm_status gdelta_step(float *state, const void *q, const void *k, const void 
  * the token pairs j < t <= i), not a difference of cumulative sums: strongly
  * forgetting gates keep its accuracy.
  *
- * workspace: gdelta_bwd_workspace_size() bytes, 256-byte aligned (the states at the
- * chunks' starts and their gradients, 8 DK DV bytes per chunk and value head, and
- * 8 DV bytes per token and value head make up most of it).
+ * workspace: gdelta_bwd_workspace_size() bytes, 256-byte aligned, not shared by two
+ * calls in flight (the states at the chunks' starts and their gradients, 8 DK DV bytes
+ * per chunk and value head, and 8 DV bytes per token and value head make up most of
+ * it).  Accuracy on the tensor-core path: dg and dbeta about 1e-6 off an fp64
+ * evaluation of the same inputs.
  */
 size_t gdelta_bwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, mlstm_dtype dt);
 mlstm_status gdelta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,

@@ -54,7 +54,9 @@ def gd(lib, fn, **over):
     (dict(beta=None), INVALID), (dict(q=FAKE + 8), INVALID), (dict(v=FAKE + 2), INVALID), (dict(B=-1), INVALID),
     (dict(NH=0), INVALID), (dict(NHV=3), INVALID), (dict(NHV=0), INVALID), (dict(dt=2), UNSUPPORTED),
     (dict(DK=12), UNSUPPORTED), (dict(DK=136), UNSUPPORTED), (dict(DV=520), UNSUPPORTED), (dict(DV=4), UNSUPPORTED),
-    (dict(DK=0), UNSUPPORTED), (dict(B=40000), UNSUPPORTED)]] + [
+    (dict(DK=0), UNSUPPORTED), (dict(B=1 << 29), UNSUPPORTED)]] + [
+    ("fwd", dict(B=40000), UNSUPPORTED), ("bwd", dict(B=40000), UNSUPPORTED),
+    ("fwd", dict(B=8000, S=1 << 30), UNSUPPORTED), ("bwd", dict(B=8000, S=1 << 30), UNSUPPORTED),
     ("fwd", dict(o=None), INVALID), ("fwd", dict(S0=FAKE + 4), INVALID), ("fwd", dict(Sf=FAKE + 8), INVALID),
     ("fwd", dict(lengths=FAKE + 2), INVALID), ("fwd", dict(S=-1), INVALID), ("fwd", dict(ws=None), WORKSPACE),
     ("fwd", dict(wsb=1000), WORKSPACE), ("fwd", dict(ws=FAKE + 16), INVALID),

@@ -427,14 +427,22 @@ def gdelta_workspace_size(B, NH, NHV, S, DK, DV, dtype, backward: bool = False) 
     return int(size(B, NH, NHV, S, DK, DV, dt))
 
 
-def _gdelta_workspace(workspace, sizes, device, index, backward):
+def _scratch(n, device, stream):
+    """A workspace for one call; on a stream of the caller's its memory outlives the call's work there."""
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    if stream is not None and n:
+        t.record_stream(stream)
+    return t
+
+
+def _gdelta_workspace(workspace, sizes, device, index, backward, stream):
     if workspace is None:
         lib = load()
         fn = "gdelta_bwd_workspace_size" if backward else "gdelta_fwd_workspace_size"
         n = int(getattr(lib, fn)(*sizes))
         if n == 0:
             raise MlstmError(fn, 2, lib)
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        return _scratch(n, device, stream)
     _need("workspace", workspace, workspace.shape, torch.uint8, index)
     return workspace
 
@@ -461,7 +469,7 @@ def gdelta_fwd(q, k, v, g, beta, state=None, lengths=None, scale=None, o_out=Non
         _need("state_out", state_out, (B, NHV, DK, DV), torch.float32, index)
     elif return_state:
         state_out = torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device)
-    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, False)
+    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, False, stream)
     _check("gdelta_fwd", _on(index, stream, lambda s: lib.gdelta_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), dt, B, NH, NHV, S, DK,
         DV, DK ** -0.5 if scale is None else scale, _addr(state), o_out.data_ptr(), _addr(state_out),
@@ -505,7 +513,7 @@ def gdelta_bwd(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scal
         if out[5] is not None:
             _need("dstate0", out[5], (B, NHV, DK, DV), torch.float32, index)
     dq, dk, dv, dg, dbeta, dstate0 = out
-    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, True)
+    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, True, stream)
     _check("gdelta_bwd", _on(index, stream, lambda s: lib.gdelta_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), _addr(state),
         do.data_ptr(), _addr(dstate), dt, B, NH, NHV, S, DK, DV, DK ** -0.5 if scale is None else scale, dq.data_ptr(),
@@ -603,7 +611,7 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm: str = "
     dwk = None if k_weight is None else torch.empty_like(k_weight)
     if workspace is None:
         n = int(lib.qknorm_bwd_workspace_size(B, S, NHQ, NHK, D)) if (dwq is not None or dwk is not None) else 0
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     else:
         _need("workspace", workspace, workspace.shape, torch.uint8, index)
     _check("qknorm_bwd", _on(index, stream, lambda s: lib.qknorm_bwd(

@@ -13,12 +13,21 @@ namespace {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-mlstm_status check_shape(mlstm_dtype dt, int B, int NH, int NHV, int S, int DK, int DV)
+mlstm_status check_heads(mlstm_dtype dt, int B, int NH, int NHV, int DK, int DV)
 {
-    if (B < 0 || S < 0 || NH < 1 || NHV < 1 || NHV % NH != 0) return MLSTM_ERR_INVALID_ARG;
+    if (B < 0 || NH < 1 || NHV < 1 || NHV % NH != 0) return MLSTM_ERR_INVALID_ARG;
     if (dt != MLSTM_F32 && dt != MLSTM_BF16) return MLSTM_ERR_UNSUPPORTED;
     if (DK < 8 || DK > 128 || DK % 8 != 0 || DV < 8 || DV > 512 || DV % 8 != 0) return MLSTM_ERR_UNSUPPORTED;
+    return MLSTM_OK;
+}
+
+mlstm_status check_shape(mlstm_dtype dt, int B, int NH, int NHV, int S, int DK, int DV)
+{
+    if (S < 0) return MLSTM_ERR_INVALID_ARG;
+    const mlstm_status st = check_heads(dt, B, NH, NHV, DK, DV);
+    if (st != MLSTM_OK) return st;
     if ((long long)B * NHV > 65535 || S > (1 << 30)) return MLSTM_ERR_UNSUPPORTED;
+    if ((long long)B * NHV * (S / CH + 1) > 0x7fffffffll) return MLSTM_ERR_UNSUPPORTED;   // chunks, counted in an int
     return MLSTM_OK;
 }
 
@@ -144,8 +153,9 @@ mlstm_status gdelta_step(float *state, const void *q, const void *k, const void 
                          const float *beta, mlstm_dtype dt, int B, int NH, int NHV, int DK, int DV, float scale,
                          void *o, void *stream)
 {
-    const mlstm_status st = check_shape(dt, B, NH, NHV, 1, DK, DV);
+    const mlstm_status st = check_heads(dt, B, NH, NHV, DK, DV);
     if (st != MLSTM_OK) return st;
+    if ((long long)B * NHV * (DV / 8) > 0x7fffffffll) return MLSTM_ERR_UNSUPPORTED;   // CTAs, at most one for 8 columns
     if (B == 0) return MLSTM_OK;
     if (!state || !q || !k || !v || !g || !beta || !o) return MLSTM_ERR_INVALID_ARG;
     if (!aligned16(state) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned4(g) ||

@@ -21,6 +21,7 @@
 #include "tc_fwd.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace mlstm {
 namespace gdelta {
@@ -52,7 +53,12 @@ static_assert(MH + 64 * LDM * 4 <= GA, "the pairs' matrices fit over the operand
 static_assert(TOTAL <= 232448, "one CTA's shared memory");
 
 // TMEM columns
-constexpr uint32_t CZ = 0, CW = 128, CH_ = 256, CD = 320;
+constexpr uint32_t CZ = 0, CW = 128, CH_ = 256, CD = 320, CHS = 448;   // CHS: HX's products of the smaller parts
+// An MMA cuts its sum off where fp32 ends, always towards zero, and every one of them adds to the error: HX keeps
+// its largest products apart from the others, and Z and W go to the threads' registers, whose additions round,
+// after SUM stages.  After every stage, 128 value columns take 535 us where they take 470, for a dg 8e-7 off fp64
+// either way; never, 256 columns are 1.4e-6 off.
+constexpr int SUM = 2;
 
 struct Params {
     const __nv_bfloat16 *d_o;
@@ -103,15 +109,22 @@ MLSTM_DEVINL void store2(uint8_t *tile, uint32_t row, uint32_t j0, const float (
     }
 }
 
-MLSTM_DEVINL void ld32(uint32_t taddr, float (&x)[32])
+// N accumulator columns at a time: between two stages, with their operands in registers, or behind the last
+using Few = std::integral_constant<int, 16>;
+using All = std::integral_constant<int, 32>;
+
+template <int N>
+MLSTM_DEVINL void ld(uint32_t taddr, float (&x)[N])
 {
-    uint32_t r[32];
-    tmem_ld32(taddr, r);
+    uint32_t r[N];
+    if constexpr (N == 16) tmem_ld16(taddr, r);
+    else tmem_ld32(taddr, r);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
 }
 
+template <bool LONG>   // more than SUM stages
 __global__ void __launch_bounds__(THREADS, 1)
 grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const Params p)
 {
@@ -195,14 +208,14 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_ss(tmem + CZ, da + (uint64_t)(PA[q] * 1024 + k * 2), ds + (uint64_t)(PB[q] * 1024 + k * 2), IDN,
-                                       s + q + k > 0);
+                                       s % SUM + q + k > 0);
                         mbar_wait(e_ready, n & 1u, wc);
 #pragma unroll
                         for (int q = 0; q < 6; ++q)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_ss(tmem + CH_, da + (uint64_t)(PA[q] * 1024 + k * 2), de + (uint64_t)(PB[q] * 512 + k * 2), IDH,
-                                       s + q + k > 0);
+                                mma_ss(tmem + (q < 5 ? CHS : CH_), da + (uint64_t)(PA[q] * 1024 + k * 2), de + (uint64_t)(PB[q] * 512 + k * 2), IDH,
+                                       s + q % 5 + k > 0);
                         mma_commit(z_done);   // and HX: [dO; dV] and S are free
                         mbar_wait(d_ready, n & 1u, wc);
                         // E in rows 64..127; the rows in front of a part read what lies before it, into lanes nothing uses
@@ -211,7 +224,7 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
                                 mma_ss(tmem + CW, de + (uint64_t)(PA[q] * 512 - 512 + k * 2), dd + (uint64_t)(PB[q] * 1024 + k * 2), IDN,
-                                       s + q + k > 0);
+                                       s % SUM + q + k > 0);
                         mma_commit(w_done);
                     }
                     asm volatile("" : "+l"(a1), "+l"(bk), "+l"(pt), "+l"(pt2), "+l"(at), "+l"(at2));
@@ -320,9 +333,49 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     ga[tid] = make_float4(gx.x, gx.y, bt, exp2f(gx.x + gx.y));
                     go[tid] = exp2f((gl.x - gx.x) + (gl.y - gx.y));
                 }
+                // SUM stages' Z and W, 64 columns of the thread's row: onto dq or dk, and their products with q or k.
+                float zin = 0.f, zout = 0.f;
+                auto fold = [&](auto width, uint32_t tcol, float f, float &sum) {
+                    constexpr int N = decltype(width)::value;
+#pragma unroll
+                    for (int cc = 0; cc < 64 / N; ++cc) {
+                        float z[N];
+                        ld<N>(tl + tcol + half * 64 + cc * N, z);
+#pragma unroll
+                        for (int j = 0; j < N / 8; ++j) {   // row t of K (dk) or Q (dq)
+                            const uint4 u = *reinterpret_cast<const uint4 *>(
+                                smem + KQ + sw128_chunk(top ? 64 + t : t, half * 8 + cc * (N / 8) + j, 128));
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float z0 = z[8 * j + 2 * e], z1 = z[8 * j + 2 * e + 1];
+                                const float2 x = unpack_bf16((&u.x)[e]);
+                                sum = fmaf(z0, x.x, sum);
+                                sum = fmaf(z1, x.y, sum);
+                                uint64_t &a = acc[cc * (N / 2) + 4 * j + e];
+                                a = f2_fma(f2_pack(f, f), f2_pack(z0, z1), a);
+                            }
+                        }
+                    }
+                };
+                auto fz = [&] { return top ? p.scale * ga[t].w : -ga[t].w; };
+                auto take_kq = [&] {   // K and Q: their padding rows would meet zeros, which NaN survives
+                    mbar_wait(kq_full, it & 1u, wc);
+                    ++it;
+                    if (t >= len) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(smem + KQ + sw128_chunk(row, half * 8 + j, 128)) = zero;
+                    }
+                };
                 float sd = 0.f;
                 for (int s = 0; s < nst; ++s, ++n) {
-                    if (s > 0) mbar_wait(z_done, (n - 1) & 1u, wc);
+                    if (s > 0) {
+                        mbar_wait(z_done, (n - 1) & 1u, wc);
+                        if (LONG && s % SUM == 0) {
+                            if (h == 0 && s == SUM) take_kq();
+                            tc_fence_after();
+                            fold(Few{}, CZ, fz(), zin);
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int r = u0 + 32 * k;
@@ -337,7 +390,13 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     for (int k = 0; k < 4; ++k) put(TS, 16384, u0 + 32 * k, 128, rs[k]);
                     load_state(Dg, s * 64, rd);
                     arrive(as_ready);
-                    if (s > 0) mbar_wait(w_done, (n - 1) & 1u, wc);
+                    if (s > 0) {
+                        mbar_wait(w_done, (n - 1) & 1u, wc);
+                        if (LONG && s % SUM == 0 && !top) {
+                            tc_fence_after();
+                            fold(Few{}, CW, go[t] * ga[t].z, zout);
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < 2; ++k) put(TE, 8192, u0 + 32 * k, 64, re[k]);
                     arrive(e_ready);
@@ -357,14 +416,7 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 sd = warp_sum(sd);
                 if (lane == 0) sds[warp] = sd;
-                if (h == 0) {   // K and Q: their padding rows would meet zeros, which NaN survives
-                    mbar_wait(kq_full, it & 1u, wc);
-                    ++it;
-                    if (t >= len) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4 *>(smem + KQ + sw128_chunk(row, half * 8 + j, 128)) = zero;
-                    }
-                }
+                if (h == 0 && (!LONG || nst <= SUM)) take_kq();
                 // P's or KK's entries of the thread's row, asked for while the last products run; and the next
                 // head's operands, or the next chunk's, to L2
                 const int j0 = 32 * half;
@@ -406,51 +458,22 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 mbar_wait(z_done, (n - 1) & 1u, wc);
                 mbar_wait(w_done, (n - 1) & 1u, wc);
                 tc_fence_after();
+                fold(All{}, CZ, fz(), zin);
+                if (!top) fold(All{}, CW, go[t] * ga[t].z, zout);
+                zi[(half * 2 + (top ? 0 : 1)) * 64 + t] = t < len ? fz() * zin : 0.f;
+                if (!top) zo[half * 64 + t] = t < len ? go[t] * zout : 0.f;
                 const float4 gt = ga[t];
-                {   // the inter-chunk terms: 64 columns of Z and, for dk, of W, and their products with q and k
-                    const float fz = top ? p.scale * gt.w : -gt.w, fw = go[t];
-                    float zin = 0.f, zout = 0.f;
-#pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
-                        float z[32];
-                        ld32(tl + CZ + half * 64 + cc * 32, z);
-                        // row t of K (dk) or Q (dq)
-                        float qk[32];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint4 u = *reinterpret_cast<const uint4 *>(smem + KQ + sw128_chunk(top ? 64 + t : t, half * 8 + cc * 4 + j, 128));
-                            const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 f = unpack_bf16(uu[e]);
-                                qk[8 * j + 2 * e] = f.x;
-                                qk[8 * j + 2 * e + 1] = f.y;
-                            }
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            zin = fmaf(z[e], qk[e], zin);
-                            zin = fmaf(z[e + 1], qk[e + 1], zin);
-                            acc[cc * 16 + e / 2] = f2_fma(f2_pack(fz, fz), f2_pack(z[e], z[e + 1]), acc[cc * 16 + e / 2]);
-                        }
-                        if (!top) {
-                            ld32(tl + CW + half * 64 + cc * 32, z);
-                            const float f = fw * gt.z;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                zout = fmaf(z[e], qk[e], zout);
-                                zout = fmaf(z[e + 1], qk[e + 1], zout);
-                                acc[cc * 16 + e / 2] = f2_fma(f2_pack(f, f), f2_pack(z[e], z[e + 1]), acc[cc * 16 + e / 2]);
-                            }
-                        }
-                    }
-                    zi[(half * 2 + (top ? 0 : 1)) * 64 + t] = t < len ? fz * zin : 0.f;
-                    if (!top) zo[half * 64 + t] = t < len ? fw * zout : 0.f;
-                }
                 // the pairs: row t, columns j0 .. j0 + 31.  The operands' tiles are no longer read
                 {
                     float x[32];
-                    ld32(tl + CH_ + j0, x);
+                    {
+                        uint32_t r0[32], r1[32];
+                        tmem_ld32(tl + CH_ + j0, r0);
+                        tmem_ld32(tl + CHS + j0, r1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(r0[e]) + __uint_as_float(r1[e]);
+                    }
                     float *m1 = (top ? mz : mh) + t * LDM + j0;
                     const float f = top ? p.scale : -1.f;
                     const int lim = top ? t : t - 1;   // P's columns j <= t, KK's j < t
@@ -481,9 +504,9 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 if (s4 == 0 && r < len) p.dbeta[vrow + r] = sum + zo[r] + zo[64 + r];
-                float zin = 0.f, zob = 0.f;   // of token tid
+                float zis = 0.f, zob = 0.f;   // of token tid
                 if (tid < 64) {
-                    zin = (zi[tid] + zi[64 + tid]) + (zi[128 + tid] + zi[192 + tid]);
+                    zis = (zi[tid] + zi[64 + tid]) + (zi[128 + tid] + zi[192 + tid]);
                     zob = ga[tid].z * (zo[tid] + zo[64 + tid]);
                 }
                 sync();
@@ -504,7 +527,7 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int e = 0; e < 16; ++e) mz[r * LDM + s4 * 16 + e] = before + z16[e];
                 if (tid < 64) {
-                    zi[tid] = zin;
+                    zi[tid] = zis;
                     zi[64 + tid] = zob;
                 }
                 sync();
@@ -530,7 +553,7 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
                 float z[32];
-                ld32(tl + CD + half * 64 + cc * 32, z);
+                ld<32>(tl + CD + half * 64 + cc * 32, z);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t o[4];
@@ -561,14 +584,15 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 cudaError_t launch_grad_tc(const Args &a, const Workspace &w, const Maps &m, const void *d_o, void *dq, void *dk,
                            float *dg, float *dbeta)
 {
-    cudaError_t e = ensure_dynamic_smem((const void *)grad_tc_kernel, TOTAL);
+    auto kernel = a.DV > 64 * SUM ? grad_tc_kernel<true> : grad_tc_kernel<false>;
+    cudaError_t e = ensure_dynamic_smem((const void *)kernel, TOTAL);
     if (e != cudaSuccess) return e;
     Params p = {static_cast<const __nv_bfloat16 *>(d_o), a.beta, a.lengths, static_cast<__nv_bfloat16 *>(dq),
                 static_cast<__nv_bfloat16 *>(dk), dg, dbeta, a.B, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w};
     int sms = 0;
     if ((e = sm_count(&sms)) != cudaSuccess) return e;
     const long long items = (long long)w.NC * a.B * a.NH;
-    return launch_kernel(grad_tc_kernel, dim3((unsigned)std::min<long long>(items, sms)), dim3(THREADS), TOTAL, a.stream, 1,
+    return launch_kernel(kernel, dim3((unsigned)std::min<long long>(items, sms)), dim3(THREADS), TOTAL, a.stream, 1,
                          m.q, m.k, p);
 }
 

@@ -16,9 +16,10 @@
 // the same tile, read MN-major, is the A operand of the state's update.  The fp32 operands S, Y and the
 // state update's enter as three bf16 parts each, which hold all 24 bits, side by side along N: one MMA
 // reads A once for all three, and the epilogue adds the parts' columns.  T - I and G enter as two parts,
-// value and rounding residue (rms error 2.7e-6 of the correction they carry); K, Q, dO are exact.  Without
-// its unit diagonal T leaves Y itself out of the MMA: the threads that formed Y in fp32 add it to the
-// result.  The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
+// value and rounding residue (rms error 2.7e-6 of the correction they carry), T - I in the backward's forward
+// walk as three: dg and dbeta are fp32 outputs, and two parts alone put 4e-7 (DK 128) to 7e-7 (DK 64) into dg
+// through E, against 1e-7 through dV.  K, Q, dO are exact.  Without its unit diagonal T leaves Y itself out of the
+// MMA: the threads that formed Y in fp32 add it to the result.  The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
 // each, and takes the update with fp32 additions.
 //
 // Roles: warp 0 one TMA thread, warp 1 the MMA thread (and the TMEM allocation), then 4 epilogue warps per
@@ -345,6 +346,17 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
                     *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
+                    if (w.TL && part == 0) {   // the backward's third part of T - I
+                        float z[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t h = hi[e >> 1], l = lo[e >> 1];
+                            z[e] = (y[e] - __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16)) -
+                                   __uint_as_float(e & 1 ? l & 0xffff0000u : l << 16);
+                        }
+                        *reinterpret_cast<uint2 *>(w.TL + ch * 8192 + sw128_offset(i0 + r, c0, 64)) =
+                            make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
+                    }
                 }
             }
             __syncthreads();
@@ -372,7 +384,10 @@ struct Walk {
     static constexpr int EPI = 4 * (CW / 16);              // epilogue warps per chain, 16 columns each
     static constexpr int THREADS = 64 + 32 * NCH * EPI;
     static constexpr int STAGES = 2;
-    static constexpr uint32_t STAGE = 65536;               // [K; Q] 32 KB, [T - I; G] values and residues 16 KB each
+    // [K; Q] 32 KB, [T - I; G] values and residues 16 KB each.  KEEP has no use for Q and G, whose lanes' sums stay
+    // unread: K alone, with Q's place left as it is, and three parts of T - I, 8 KB each
+    static constexpr uint32_t STAGE = MODE == KEEP ? 57344 : 65536;
+    static constexpr uint32_t LOADED = MODE == KEEP ? 40960 : 65536;
     static constexpr uint32_t BLOCKS = (3 * CW + 63) / 64; // blocks of 64 columns that hold an operand's parts
     static constexpr uint32_t SP = STAGES * STAGE;         // per chain: S parts, 128 rows
     static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
@@ -462,12 +477,19 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int st = c % NST, ci = MODE == REVERSE ? nc - 1 - c : c;
                 if (c >= NST && !mbar_wait(&empty[st], (uint32_t)(c / NST - 1) & 1u, wc)) break;
                 uint8_t *s = smem + st * W::STAGE;
-                mbar_arrive_expect_tx(&full[st], W::STAGE);
+                mbar_arrive_expect_tx(&full[st], W::LOADED);
                 for (int kb = 0; kb < 2; ++kb) {
                     tma_load_3d(s + kb * 16384, &tm_k, 64 * kb, ci * CH, bh, &full[st]);
-                    tma_load_3d(s + kb * 16384 + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
+                    if (MODE != KEEP) tma_load_3d(s + kb * 16384 + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
                 }
-                bulk_load(s + 32768, p.w.TG + ((size_t)bhv * p.w.NC + ci) * 32768, 32768, &full[st]);
+                const size_t ch = (size_t)bhv * p.w.NC + ci;
+                if (MODE == KEEP) {
+                    bulk_load(s + 32768, p.w.TG + ch * 32768, 8192, &full[st]);
+                    bulk_load(s + 40960, p.w.TG + ch * 32768 + 16384, 8192, &full[st]);
+                    bulk_load(s + 49152, p.w.TL + ch * 8192, 8192, &full[st]);
+                } else {
+                    bulk_load(s + 32768, p.w.TG + ch * 32768, 32768, &full[st]);
+                }
             }
         }
     } else if (warp == 1) {
@@ -478,6 +500,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             constexpr uint32_t IDD = idesc_bf16(128, 3 * CW, 1, 1);
             constexpr uint32_t BS = W::BLOCKS * 1024, BY = W::BLOCKS * W::YROWS * 8;   // a chain's operands, 16-byte units
             // reverse: T^T and G^T, M = 64; the 64 M behind read what lies behind, into lanes that nothing uses
+            constexpr uint32_t IDG0 = idesc_bf16(128, CW, 0, 1), RES = MODE == KEEP ? 512 : 1024;
             constexpr uint32_t IDTM = idesc_bf16(128, 2 * CW, 1, 1), IDG = idesc_bf16(128, CW, 1, 1);
             const uint64_t atm = smem_desc(smem_u32(smem) + 32768, 8192, 1024);
             const uint64_t bo = MODE == REVERSE ? smem_desc(smem_u32(smem + W::DO), 8192, 1024) : 0;
@@ -522,8 +545,13 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDD : IDX, k > 0);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
-                        mma_ss(de, MODE == REVERSE ? atm + so + (uint64_t)(1024 + k * 128) : at + so + (uint64_t)(1024 + k * 2),
+                        mma_ss(de, MODE == REVERSE ? atm + so + (uint64_t)(1024 + k * 128) : at + so + (uint64_t)(RES + k * 2),
                                by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDTM : IDM, 1);
+                    if (MODE == KEEP) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)   // the third part of T - I with Y's first
+                            mma_ss(de, at + so + (uint64_t)(2 * RES + k * 2), by + (uint64_t)(h * BY + k * 128), IDG0, 1);
+                    }
                     mma_commit(&e_done[h]);
                 };
                 auto issue_d = [&](int h) {

@@ -20,7 +20,8 @@
  * Conventions are those of mlstm.h: device pointers owned by the caller, contiguous,
  * row-major, 16-byte aligned; work is enqueued on `stream` and nothing synchronizes;
  * bad arguments return an error status before anything is enqueued; the library
- * allocates nothing.  Layouts:
+ * allocates nothing.  No output may overlap an input or another output, but for the
+ * states that a function's comment names.  Layouts:
  *   q, k [B][NH][S][DK]; v, o [B][NHV][S][DV]  in the element type `dt`;
  *   g, beta [B][NHV][S] float32; states [B][NHV][DK][DV] float32.
  * NHV is a multiple of NH: value head h reads query and key head h / (NHV / NH).

@@ -20,8 +20,8 @@
  * of all of them.  D a multiple of 8 in [8, 512]; RD even in [0, D] (0: no rotation).
  * positions: device int32 [B][S], or NULL for 0 .. S-1; inv_freq: device float32 [RD / 2].
  * NHQ or NHK may be 0 (that side's pointers are not looked at), at most 4096; B * S < 2^31.
- * Strides of inputs may be 0 or overlap; strides of outputs may not.  Other conventions
- * as in mlstm.h.
+ * Strides of inputs may be 0 or overlap; strides of outputs may not, and no output may
+ * overlap an input.  Other conventions as in mlstm.h.
  */
 #ifndef QKNORM_H
 #define QKNORM_H

@@ -345,3 +345,76 @@ def test_long_and_wide(B, NH, NHV, S):
     x = make(B, NH, NHV, S, 128, 128, "bf16", seed=50, rate=0.01)
     check_fwd(x, state=True)
     check_bwd(x, state=True)
+
+
+@pytest.mark.parametrize("DK,DV,NH,NHV", [(64, 320, 1, 3), (128, 256, 2, 2), (96, 512, 1, 2)])
+def test_many_value_columns(DK, DV, NH, NHV):
+    """Up to eight stages of 64 value columns in the gradients, several heads of a group, items of every length."""
+    x = make(5, NH, NHV, 150, DK, DV, "bf16", seed=60, rate=0.3)
+    lengths = torch.tensor([150, 0, 64, 1, 129], dtype=torch.int32, device="cuda")
+    check_fwd(x, state=True, lengths=lengths)
+    check_bwd(x, state=True, dstate=True, lengths=lengths)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_resets_side_by_side_and_growing_gates(dt):
+    """Resets at neighbouring tokens, at a chunk's first and last token, and gates above zero in between."""
+    x = make(1, 1, 2, 200, 64, 64, dt, seed=61, rate=0.2)
+    x["g"][..., 70:90] = 0.05
+    x["g"][..., [0, 10, 11, 12, 63, 64, 127, 128, 199]] = -torch.inf
+    check_fwd(x, state=True)
+    check_bwd(x, state=True, dstate=True)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_nothing_left_in_a_workspace_is_read(dt):
+    x = make(3, 1, 2, 150, 64, 64, dt, seed=62)
+    lengths = torch.tensor([150, 70, 0], dtype=torch.int32, device="cuda")
+    n = binding.gdelta_workspace_size(3, 1, 2, 150, 64, 64, x["q"].dtype, backward=True)
+    runs = []
+    for fill in (0, 0xff):   # 0xff: NaN of either type
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        a = binding.gdelta_fwd(*args(x), lengths=lengths, workspace=ws)
+        ws.fill_(fill)
+        runs.append((*a, *binding.gdelta_bwd(*args(x), x["do"], state=x["S0"], lengths=lengths, workspace=ws)))
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+
+
+def test_states_in_place():
+    x = make(2, 2, 4, 100, 128, 64, "bf16", seed=63)
+    o, S = binding.gdelta_fwd(*args(x), state=x["S0"])
+    own = x["S0"].clone()
+    o2, S2 = binding.gdelta_fwd(*args(x), state=own, state_out=own)
+    assert S2 is own and torch.equal(S, own) and torch.equal(o, o2)
+    ref = binding.gdelta_bwd(*args(x), x["do"], state=x["S0"], dstate=x["dS"])
+    d = x["dS"].clone()
+    out = tuple(torch.empty_like(t) for t in args(x)) + (d,)
+    got = binding.gdelta_bwd(*args(x), x["do"], state=x["S0"], dstate=d, out=out)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+
+
+def test_calls_in_flight_on_two_streams():
+    """Given streams, workspaces allocated inside: calls run side by side and their memory is not handed on early."""
+    xs = [make(2, 2, 2, 300, 128, 128, "bf16", seed=s) for s in (64, 65)]
+    ref = [(*binding.gdelta_fwd(*args(x)), *binding.gdelta_bwd(*args(x), x["do"])[:5]) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = [(*binding.gdelta_fwd(*args(x), stream=s), *binding.gdelta_bwd(*args(x), x["do"], stream=s)[:5])
+               for x, s in zip(xs, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            assert all(torch.equal(u, w) for u, w in zip(a, b))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_step_of_more_heads_than_a_grid_axis_holds(dt):
+    x = make(35000, 1, 2, 1, 8, 8, dt, seed=66)
+    tok = [t[:, :, 0].contiguous() for t in args(x)]
+    S = x["S0"].clone()
+    o = binding.gdelta_step(S, *tok)
+    ro, rS = oracle.gdelta_fwd(*args(x), state=x["S0"])
+    assert_close("o", o, ro[:, :, 0], tol(o))
+    assert_close("state", S, rS, F32)

@@ -464,7 +464,7 @@ mlstm_status check(const Params &p, mlstm_dtype dt, int NHQ, int NHK, qknorm_kin
 
 Side make_side(const void *x, qknorm_strides xs, const void *dy, void *out, qknorm_strides os, const float *w, int heads)
 {
-    Side s = {x, dy, out, w, xs, os, heads};
+    Side s = {x, dy, out, heads ? w : nullptr, xs, os, heads};   // without heads nothing of a side is read
     return s;
 }
 

@@ -18,12 +18,19 @@
 // 16-byte shared-memory loads with the reduction index outermost; what bounds these kernels is the
 // CUDA cores' fp32 rate and, for few heads, the chain of three products per chunk.
 #include "gdelta_prep.cuh"
+#include "tc_common.cuh"
 
 #include <algorithm>
 
 namespace mlstm {
 namespace gdelta {
 namespace {
+
+using tc::f2_fma;
+using tc::f2_mul;
+using tc::f2_pack;
+using tc::f2_unpack;
+using tc::smem_u32;
 
 constexpr int LDR = 132;   // row stride of [.][128] tiles
 constexpr int VT = 32;     // value columns of a walk CTA
@@ -118,155 +125,265 @@ prep_kernel(const T *__restrict__ q, const T *__restrict__ k, const float *__res
     }
 }
 
-// ---------------------------------------------------------------- forward walk
+// ---------------------------------------------------------------- walks
+//
+// A CTA of 256 threads runs one value head's chunks over 32 value columns; thread (u = tid / 8, tid % 8) owns the
+// tokens 2 u and 2 u + 1 and the state's rows 4 u .. 4 u + 3, four columns each.  The state stays in registers, with
+// a copy in shared memory for the products that read all of it.  Everything is row-major as it lies in memory, so
+// that the copies are plain and asynchronous: the next chunk's K and Q arrive during the whole of this one, T and P,
+// which have no second buffer, during the state's update.
 
-constexpr size_t WALK_SMEM = sizeof(float) * (128 * LDR + 128 * VT + 2 * 64 * LDT + 64 * VT + 3 * 64);
+constexpr int LDX = 132;   // row stride of K and Q: rows 2 u .. of a warp's four u start 8 banks apart
+constexpr int LDW = 68;    // of T and P, likewise
 
-// One CTA per value head and 32 value columns; KEEP: the backward's recomputation (writes the states at
-// the chunks' starts and E, no outputs).
+struct Gates { float ea[64], eo[64], bt[64]; };
+
+struct WalkSmem {
+    float kq[2][128 * LDX];            // K over Q
+    float t[64 * LDW], p[64 * LDW];
+    float st[128 * VT];                // the state, or its gradient
+    float y[64 * VT], z[64 * VT];      // forward: Y, then U; e^{a_64 - a} U.  Reverse: beta dU; -e^a dV
+    float x[64 * VT];                  // reverse: dO, then scale e^a dO
+    Gates g[2];
+};
+static_assert(sizeof(WalkSmem) <= 232448, "one CTA's shared memory");
+
+MLSTM_DEVINL void copy16(float *dst, const float *src, bool on)   // off: zeros
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+MLSTM_DEVINL void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Rows of src (row stride DK, `len` of them live, zeros behind) to dst [64][LDX].
+MLSTM_DEVINL void stage_rows(const float *src, int len, int DK, float *dst, int tid)
+{
+    const int d = (tid & 31) * 4;
+    if (d < DK)
+        for (int r = tid >> 5; r < 64; r += 8) copy16(dst + r * LDX + d, src + (r < len ? (size_t)r * DK + d : 0), r < len);
+}
+MLSTM_DEVINL void stage_rows(const __nv_bfloat16 *src, int len, int DK, float *dst, int tid)
+{
+    const int d = (tid & 31) * 4;
+    if (d < DK)
+        for (int r = tid >> 5; r < 64; r += 8)
+            st4(dst + r * LDX + d, r < len ? load4(src + (size_t)r * DK + d) : make_float4(0.f, 0.f, 0.f, 0.f));
+}
+MLSTM_DEVINL void stage64(const float *src, float *dst, int tid)
+{
+    for (int i = tid; i < 64 * 16; i += 256) copy16(dst + (i >> 4) * LDW + (i & 15) * 4, src + i * 4, true);
+}
+
+// A chunk's gates, read by thread t < 64 one chunk ahead.
+struct GateReg {
+    float2 a, last;
+    float b;
+    MLSTM_DEVINL void read(const Workspace &w, const float *beta, size_t ch, size_t vrow, int len, int t)
+    {
+        a = w.A[ch * 64 + t];
+        last = w.A[ch * 64 + 63];
+        b = t < len ? beta[vrow + t] : 0.f;
+    }
+    MLSTM_DEVINL void put(Gates &g, int t) const
+    {
+        g.ea[t] = expf(a.x + a.y);
+        g.eo[t] = expf(gate_diff(last, a));
+        g.bt[t] = b;
+    }
+};
+
+// Four columns as two packed pairs.
+struct Row4 { uint64_t a, b; };
+MLSTM_DEVINL Row4 ldr(const float *p)
+{
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
+    return Row4{v.x, v.y};
+}
+MLSTM_DEVINL void str(float *p, Row4 v) { *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(v.a, v.b); }
+MLSTM_DEVINL Row4 row4(float4 v) { return Row4{f2_pack(v.x, v.y), f2_pack(v.z, v.w)}; }
+MLSTM_DEVINL float4 flat(Row4 v)
+{
+    const float2 a = f2_unpack(v.a), b = f2_unpack(v.b);
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+MLSTM_DEVINL Row4 fma_row(float f, Row4 x, Row4 c)
+{
+    const uint64_t ff = f2_pack(f, f);
+    return Row4{f2_fma(ff, x.a, c.a), f2_fma(ff, x.b, c.b)};
+}
+MLSTM_DEVINL Row4 mul_row(float f, Row4 x)
+{
+    const uint64_t ff = f2_pack(f, f);
+    return Row4{f2_mul(ff, x.a), f2_mul(ff, x.b)};
+}
+
+// acc[r] += sum_{l in [l0, l1)} A[r][l] B[l], rows A of stride lda, B [.][VT] at the thread's columns; l0, l1
+// multiples of 4.
+template <int R>
+MLSTM_DEVINL void rows_times(const float *A, int lda, const float *B, int l0, int l1, Row4 (&acc)[R])
+{
+#pragma unroll 2
+    for (int l = l0; l < l1; l += 4) {
+        float4 a[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) a[r] = ld4(A + r * lda + l);
+        const Row4 b0 = ldr(B + l * VT), b1 = ldr(B + (l + 1) * VT), b2 = ldr(B + (l + 2) * VT), b3 = ldr(B + (l + 3) * VT);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            acc[r] = fma_row(a[r].w, b3, fma_row(a[r].z, b2, fma_row(a[r].y, b1, fma_row(a[r].x, b0, acc[r]))));
+    }
+}
+// acc[r] += sum_{l in [l0, l1)} A[l][r] B[l]: rows of A at the first of two neighbouring columns.
+MLSTM_DEVINL void cols2_times(const float *A, int lda, const float *B, int l0, int l1, Row4 (&acc)[2])
+{
+#pragma unroll 4
+    for (int l = l0; l < l1; ++l) {
+        const float2 a = *reinterpret_cast<const float2 *>(A + l * lda);
+        const Row4 b = ldr(B + l * VT);
+        acc[0] = fma_row(a.x, b, acc[0]);
+        acc[1] = fma_row(a.y, b, acc[1]);
+    }
+}
+// The state's update: four neighbouring columns of A.
+MLSTM_DEVINL void cols4_times(const float *A, int lda, const float *B, Row4 (&acc)[4])
+{
+#pragma unroll 4
+    for (int l = 0; l < 64; ++l) {
+        const float4 a = ld4(A + l * lda);
+        const Row4 b = ldr(B + l * VT);
+        acc[0] = fma_row(a.x, b, acc[0]);
+        acc[1] = fma_row(a.y, b, acc[1]);
+        acc[2] = fma_row(a.z, b, acc[2]);
+        acc[3] = fma_row(a.w, b, acc[3]);
+    }
+}
+
+// KEEP: the backward's recomputation (writes the states at the chunks' starts and E, no outputs).
 template <typename T, bool KEEP>
 __global__ void __launch_bounds__(256)
 walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
             const float *__restrict__ beta, const int *__restrict__ lengths, const float *S0, int NH, int NHV,
             int S, int DK, int DV, float scale, Workspace w, T *__restrict__ o, float *S_final)
 {
-    extern __shared__ __align__(16) float sm[];
-    float *kq = sm;                    // [DK][LDR]
-    float *st = kq + 128 * LDR;        // [DK][VT] the state
-    float *tt = st + 128 * VT;         // [64][LDT] T transposed
-    float *pt = tt + 64 * LDT;         // [64][LDT] P transposed
-    float *y = pt + 64 * LDT;          // [64][VT] Y, then U, then e^{a_64 - a} U
-    float *ea = y + 64 * VT, *eo = ea + 64, *bt = eo + 64;
+    extern __shared__ __align__(16) unsigned char raw[];
+    WalkSmem &sm = *reinterpret_cast<WalkSmem *>(raw);
+    constexpr bool ASYNC = sizeof(T) == 4;   // bf16 is widened on its way: no asynchronous copy
     const int tid = threadIdx.x, c0 = blockIdx.x * VT, bhv = blockIdx.y, b = bhv / NHV;
     const int bh = b * NH + (bhv % NHV) / (NHV / NH);
-    const int r0 = (tid >> 3) * 4, j0 = (tid & 7) * 4, col = c0 + j0;   // the thread's tile of 4 x 4
-    const bool in = col < DV, krow = r0 < 64;
+    const int u = tid >> 3, j0 = (tid & 7) * 4, col = c0 + j0, t0 = 2 * u, top = 8 * (tid >> 5) + 8;   // top: behind the warp's tokens
+    const bool in = col < DV, mine = in && 4 * u < DK;   // mine: the thread's rows of the state exist
     griddep_wait();
     griddep_launch_dependents();
-    const int n = live_tokens(lengths, b, S);
-    for (int i = tid; i < DK * 8; i += 256) {
-        const int d = i >> 3, j = (i & 7) * 4;
-        st4(st + d * VT + j, S0 && c0 + j < DV ? ld4(S0 + ((size_t)bhv * DK + d) * DV + c0 + j)
-                                               : make_float4(0.f, 0.f, 0.f, 0.f));
+    const int n = live_tokens(lengths, b, S), nc = (n + CH - 1) / CH;
+    auto stage_kq = [&](int c) {
+        const size_t at = ((size_t)bh * S + c * CH) * DK;
+        stage_rows(k + at, min(CH, n - c * CH), DK, sm.kq[c & 1], tid);
+        if (!KEEP) stage_rows(q + at, min(CH, n - c * CH), DK, sm.kq[c & 1] + 64 * LDX, tid);
+    };
+    auto stage_tp = [&](int c) {
+        const size_t at = ((size_t)bhv * w.NC + c) * 4096;
+        stage64(w.T + at, sm.t, tid);
+        if (!KEEP) stage64(w.P + at, sm.p, tid);
+    };
+    GateReg gr;
+    auto read_gates = [&](int c) {
+        if (tid < 64) gr.read(w, beta, (size_t)bhv * w.NC + c, (size_t)bhv * S + c * CH, min(CH, n - c * CH), tid);
+    };
+    Row4 s[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        s[r] = row4(S0 && mine ? ld4(S0 + ((size_t)bhv * DK + 4 * u + r) * DV + col) : make_float4(0.f, 0.f, 0.f, 0.f));
+        str(sm.st + (4 * u + r) * VT + j0, s[r]);
     }
-    for (int c = 0; c * CH < n; ++c) {
+    if (nc > 0) {
+        if (ASYNC) stage_kq(0);
+        stage_tp(0);
+        read_gates(0);
+        if (tid < 64) gr.put(sm.g[0], tid);
+    }
+    for (int c = 0; c < nc; ++c) {
         const int len = min(CH, n - c * CH);
         const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * S + c * CH;
-        __syncthreads();
-        stage_transposed(k + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 0, tid, 256);
-        if (!KEEP) stage_transposed(q + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 64, tid, 256);
-        for (int i = tid; i < 64 * 16; i += 256) {
-            const int r = i & 63, j = (i >> 6) * 4;
-            float4 x = ld4(w.T + ch * 4096 + r * 64 + j);
-            tt[(j + 0) * LDT + r] = x.x; tt[(j + 1) * LDT + r] = x.y;
-            tt[(j + 2) * LDT + r] = x.z; tt[(j + 3) * LDT + r] = x.w;
-            if (!KEEP) {
-                x = ld4(w.P + ch * 4096 + r * 64 + j);
-                pt[(j + 0) * LDT + r] = x.x; pt[(j + 1) * LDT + r] = x.y;
-                pt[(j + 2) * LDT + r] = x.z; pt[(j + 3) * LDT + r] = x.w;
-            }
-        }
-        if (tid < 64) {
-            const float2 x = w.A[ch * 64 + tid];
-            ea[tid] = expf(x.x + x.y);
-            eo[tid] = expf(gate_diff(w.A[ch * 64 + 63], x));
-            bt[tid] = tid < len ? beta[vrow + tid] : 0.f;
-        }
-        __syncthreads();
-        if (KEEP)
-            for (int i = tid; i < DK * 8; i += 256) {
-                const int d = i >> 3, j = (i & 7) * 4;
-                if (c0 + j < DV) st4(w.SC + (ch * DK + d) * DV + c0 + j, ld4(st + d * VT + j));
-            }
-        float acc[4][4] = {};   // K S (rows 0..63) and Q S (rows 64..127)
-        if (krow || !KEEP)
-            for (int d = 0; d < DK; ++d) fma4x4(acc, ld4(kq + d * LDR + r0), ld4(st + d * VT + j0));
-        if (krow) {
+        const float *kq = sm.kq[c & 1];
+        const Gates &g = sm.g[c & 1];
+        if (!ASYNC) stage_kq(c);
+        Row4 vr[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = r0 + r;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (t < len && in) {
-                    x = load4(v + (vrow + t) * DV + col);
-                    x.x -= ea[t] * acc[r][0]; x.y -= ea[t] * acc[r][1];
-                    x.z -= ea[t] * acc[r][2]; x.w -= ea[t] * acc[r][3];
-                }
-                st4(y + t * VT + j0, x);
-            }
+        for (int r = 0; r < 2; ++r)
+            vr[r] = row4(in && t0 + r < len ? load4(v + (vrow + t0 + r) * DV + col) : make_float4(0.f, 0.f, 0.f, 0.f));
+        copies_done();
+        __syncthreads();
+        if (c + 1 < nc) {
+            if (ASYNC) stage_kq(c + 1);
+            read_gates(c + 1);
         }
-        __syncthreads();
-        float e[4][4] = {};
-        if (krow)
-            for (int j = 0; j < r0 + 4; ++j) fma4x4(e, ld4(tt + j * LDT + r0), ld4(y + j * VT + j0));
-        __syncthreads();
-        if (krow) {
+        if (KEEP && mine) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = r0 + r;
-                if (KEEP && in) st4(w.E + (ch * 64 + t) * DV + col, make_float4(e[r][0], e[r][1], e[r][2], e[r][3]));
-                const float f = KEEP ? bt[t] * eo[t] : bt[t];
-                st4(y + t * VT + j0, make_float4(f * e[r][0], f * e[r][1], f * e[r][2], f * e[r][3]));
-            }
+            for (int r = 0; r < 4; ++r) st4(w.SC + (ch * DK + 4 * u + r) * DV + col, flat(s[r]));
         }
+        Row4 xk[2] = {}, xq[2] = {};
+        if (KEEP) {
+            rows_times<2>(kq + t0 * LDX, LDX, sm.st + j0, 0, DK, xk);
+        } else {   // K and Q on the same rows of the state
+            Row4 x[4] = {};
+            const float *a = kq + t0 * LDX, *bp = sm.st + j0;
+#pragma unroll 2
+            for (int l = 0; l < DK; l += 4) {
+                const float4 f[4] = {ld4(a + l), ld4(a + LDX + l), ld4(a + 64 * LDX + l), ld4(a + 65 * LDX + l)};
+                const Row4 b0 = ldr(bp + l * VT), b1 = ldr(bp + (l + 1) * VT), b2 = ldr(bp + (l + 2) * VT), b3 = ldr(bp + (l + 3) * VT);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    x[r] = fma_row(f[r].w, b3, fma_row(f[r].z, b2, fma_row(f[r].y, b1, fma_row(f[r].x, b0, x[r]))));
+            }
+            xk[0] = x[0]; xk[1] = x[1]; xq[0] = x[2]; xq[1] = x[3];
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = t0 + r;
+            str(sm.y + t * VT + j0, t < len ? fma_row(-g.ea[t], xk[r], vr[r]) : Row4{0, 0});
+        }
+        __syncthreads();
+        Row4 e[2] = {};
+        rows_times<2>(sm.t + t0 * LDW, LDW, sm.y + j0, 0, top, e);   // T is zero above its diagonal
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = t0 + r;
+            if (KEEP && in) st4(w.E + (ch * 64 + t) * DV + col, flat(e[r]));
+            e[r] = mul_row(g.bt[t], e[r]);
+            str(sm.z + t * VT + j0, mul_row(g.eo[t], e[r]));
+            if (!KEEP) str(sm.y + t * VT + j0, e[r]);
+        }
+        if (c + 1 < nc && tid < 64) gr.put(sm.g[(c + 1) & 1], tid);
         __syncthreads();
         if (!KEEP) {
-            if (!krow) {
-                float s[4][4] = {};
-                for (int j = 0; j < r0 - 60; ++j) fma4x4(s, ld4(pt + j * LDT + r0 - 64), ld4(y + j * VT + j0));
+            Row4 x[2] = {};
+            rows_times<2>(sm.p + t0 * LDW, LDW, sm.y + j0, 0, top, x);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = r0 - 64 + r;
-                    if (t < len && in)
-                        store4(o + (vrow + t) * DV + col,
-                               make_float4(scale * (ea[t] * acc[r][0] + s[r][0]), scale * (ea[t] * acc[r][1] + s[r][1]),
-                                           scale * (ea[t] * acc[r][2] + s[r][2]), scale * (ea[t] * acc[r][3] + s[r][3])));
-                }
+            for (int r = 0; r < 2; ++r) {
+                const int t = t0 + r;
+                if (in && t < len) store4(o + (vrow + t) * DV + col, flat(mul_row(scale, fma_row(g.ea[t], xq[r], x[r]))));
             }
-            __syncthreads();
-            for (int i = tid; i < 64 * 8; i += 256) {
-                float4 x = ld4(y + i * 4);
-                const float f = eo[i >> 3];
-                st4(y + i * 4, make_float4(f * x.x, f * x.y, f * x.z, f * x.w));
-            }
-            __syncthreads();
+            __syncthreads();   // P is read
         }
-        if (r0 < DK) {   // S' rows r0 .. r0 + 3 (DK is a multiple of 8)
-            float s[4][4];
-            const float f = ea[63];
+        if (c + 1 < nc) stage_tp(c + 1);
+        if (4 * u < DK) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 x = ld4(st + (r0 + r) * VT + j0);
-                s[r][0] = f * x.x; s[r][1] = f * x.y; s[r][2] = f * x.z; s[r][3] = f * x.w;
-            }
-            for (int j = 0; j < 64; j += 4) {
-                float4 kr[4];
+            for (int r = 0; r < 4; ++r) s[r] = mul_row(g.ea[63], s[r]);
+            cols4_times(kq + 4 * u, LDX, sm.z + j0, s);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) kr[r] = ld4(kq + (r0 + r) * LDR + j);
-                fma4x4(s, make_float4(kr[0].x, kr[1].x, kr[2].x, kr[3].x), ld4(y + j * VT + j0));
-                fma4x4(s, make_float4(kr[0].y, kr[1].y, kr[2].y, kr[3].y), ld4(y + (j + 1) * VT + j0));
-                fma4x4(s, make_float4(kr[0].z, kr[1].z, kr[2].z, kr[3].z), ld4(y + (j + 2) * VT + j0));
-                fma4x4(s, make_float4(kr[0].w, kr[1].w, kr[2].w, kr[3].w), ld4(y + (j + 3) * VT + j0));
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) st4(st + (r0 + r) * VT + j0, make_float4(s[r][0], s[r][1], s[r][2], s[r][3]));
+            for (int r = 0; r < 4; ++r) str(sm.st + (4 * u + r) * VT + j0, s[r]);
         }
     }
     if (KEEP) return;
-    __syncthreads();
     for (int i = tid; i < (S - n) * 8; i += 256) {   // padding
         const int j = c0 + (i & 7) * 4;
         if (j < DV) store4(o + ((size_t)bhv * S + n + (i >> 3)) * DV + j, make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    if (S_final)
-        for (int i = tid; i < DK * 8; i += 256) {
-            const int d = i >> 3, j = (i & 7) * 4;
-            if (c0 + j < DV) st4(S_final + ((size_t)bhv * DK + d) * DV + c0 + j, ld4(st + d * VT + j));
-        }
+    if (S_final && mine) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st4(S_final + ((size_t)bhv * DK + 4 * u + r) * DV + col, flat(s[r]));
+    }
 }
-
-// ---------------------------------------------------------------- reverse walk
-
-constexpr size_t REV_SMEM = sizeof(float) * (128 * LDR + 128 * VT + 2 * 64 * LDT + 3 * 64 * VT + 3 * 64);
 
 template <typename T>
 __global__ void __launch_bounds__(256)
@@ -274,131 +391,106 @@ reverse_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
                const float *__restrict__ beta, const int *__restrict__ lengths, const float *dS_final, int NH,
                int NHV, int S, int DK, int DV, float scale, Workspace w, T *__restrict__ dv, float *dS0)
 {
-    extern __shared__ __align__(16) float sm[];
-    float *kq = sm;                    // [DK][LDR]
-    float *ds = kq + 128 * LDR;        // [DK][VT] the state's gradient
-    float *tm = ds + 128 * VT;         // [64][LDT] T
-    float *pm = tm + 64 * LDT;         // [64][LDT] P
-    float *dob = pm + 64 * LDT;        // [64][VT] dO, then scale e^a dO
-    float *x = dob + 64 * VT;          // [64][VT] P^T dO, then -e^a dV
-    float *y = x + 64 * VT;            // [64][VT] beta dU
-    float *ea = y + 64 * VT, *eo = ea + 64, *bt = eo + 64;
+    extern __shared__ __align__(16) unsigned char raw[];
+    WalkSmem &sm = *reinterpret_cast<WalkSmem *>(raw);
+    constexpr bool ASYNC = sizeof(T) == 4;
     const int tid = threadIdx.x, c0 = blockIdx.x * VT, bhv = blockIdx.y, b = bhv / NHV;
     const int bh = b * NH + (bhv % NHV) / (NHV / NH);
-    const int r0 = (tid >> 3) * 4, j0 = (tid & 7) * 4, col = c0 + j0;
-    const bool in = col < DV, krow = r0 < 64;
+    const int u = tid >> 3, j0 = (tid & 7) * 4, col = c0 + j0, t0 = 2 * u, low = 8 * (tid >> 5);   // low: the warp's first token
+    const bool in = col < DV, mine = in && 4 * u < DK;
     griddep_wait();
     griddep_launch_dependents();
-    const int n = live_tokens(lengths, b, S);
-    for (int i = tid; i < DK * 8; i += 256) {
-        const int d = i >> 3, j = (i & 7) * 4;
-        st4(ds + d * VT + j, dS_final && c0 + j < DV ? ld4(dS_final + ((size_t)bhv * DK + d) * DV + c0 + j)
-                                                     : make_float4(0.f, 0.f, 0.f, 0.f));
+    const int n = live_tokens(lengths, b, S), nc = (n + CH - 1) / CH;
+    auto stage_kq = [&](int c) {
+        const size_t at = ((size_t)bh * S + c * CH) * DK;
+        stage_rows(k + at, min(CH, n - c * CH), DK, sm.kq[c & 1], tid);
+        stage_rows(q + at, min(CH, n - c * CH), DK, sm.kq[c & 1] + 64 * LDX, tid);
+    };
+    auto stage_tp = [&](int c) {
+        const size_t at = ((size_t)bhv * w.NC + c) * 4096;
+        stage64(w.T + at, sm.t, tid);
+        stage64(w.P + at, sm.p, tid);
+    };
+    GateReg gr;
+    auto read_gates = [&](int c) {
+        if (tid < 64) gr.read(w, beta, (size_t)bhv * w.NC + c, (size_t)bhv * S + c * CH, min(CH, n - c * CH), tid);
+    };
+    Row4 s[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        s[r] = row4(dS_final && mine ? ld4(dS_final + ((size_t)bhv * DK + 4 * u + r) * DV + col) : make_float4(0.f, 0.f, 0.f, 0.f));
+        str(sm.st + (4 * u + r) * VT + j0, s[r]);
     }
-    for (int c = (n + CH - 1) / CH - 1; c >= 0; --c) {
+    if (nc > 0) {
+        if (ASYNC) stage_kq(nc - 1);
+        stage_tp(nc - 1);
+        read_gates(nc - 1);
+        if (tid < 64) gr.put(sm.g[(nc - 1) & 1], tid);
+    }
+    for (int c = nc - 1; c >= 0; --c) {
         const int len = min(CH, n - c * CH);
         const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * S + c * CH;
-        __syncthreads();
-        stage_transposed(k + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 0, tid, 256);
-        stage_transposed(q + ((size_t)bh * S + c * CH) * DK, len, DK, kq, 64, tid, 256);
-        for (int i = tid; i < 64 * 16; i += 256) {
-            const int r = i >> 4, j = (i & 15) * 4;
-            st4(tm + r * LDT + j, ld4(w.T + ch * 4096 + r * 64 + j));
-            st4(pm + r * LDT + j, ld4(w.P + ch * 4096 + r * 64 + j));
-        }
-        for (int i = tid; i < 64 * 8; i += 256) {
-            const int t = i >> 3, j = (i & 7) * 4;
-            st4(dob + t * VT + j, t < len && c0 + j < DV ? load4(d_o + (vrow + t) * DV + c0 + j)
-                                                         : make_float4(0.f, 0.f, 0.f, 0.f));
-        }
-        if (tid < 64) {
-            const float2 z = w.A[ch * 64 + tid];
-            ea[tid] = expf(z.x + z.y);
-            eo[tid] = expf(gate_diff(w.A[ch * 64 + 63], z));
-            bt[tid] = tid < len ? beta[vrow + tid] : 0.f;
-        }
-        __syncthreads();
-        for (int i = tid; i < DK * 8; i += 256) {
-            const int d = i >> 3, j = (i & 7) * 4;
-            if (c0 + j < DV) st4(w.DSC + (ch * DK + d) * DV + c0 + j, ld4(ds + d * VT + j));
-        }
-        float acc[4][4] = {};   // rows 0..63: K dS'; rows 64..127: P^T dO
-        if (krow) {
-            for (int d = 0; d < DK; ++d) fma4x4(acc, ld4(kq + d * LDR + r0), ld4(ds + d * VT + j0));
-        } else {
-            for (int i = r0 - 64; i < 64; ++i) fma4x4(acc, ld4(pm + i * LDT + r0 - 64), ld4(dob + i * VT + j0));
+        const float *kq = sm.kq[c & 1];
+        const Gates &g = sm.g[c & 1];
+        if (!ASYNC) stage_kq(c);
+        Row4 dor[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                st4(x + (r0 - 64 + r) * VT + j0, make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]));
+        for (int r = 0; r < 2; ++r)
+            dor[r] = row4(in && t0 + r < len ? load4(d_o + (vrow + t0 + r) * DV + col) : make_float4(0.f, 0.f, 0.f, 0.f));
+        copies_done();
+        __syncthreads();
+        if (c > 0) {
+            if (ASYNC) stage_kq(c - 1);
+            read_gates(c - 1);
+        }
+        if (mine) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) st4(w.DSC + (ch * DK + 4 * u + r) * DV + col, flat(s[r]));
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) str(sm.x + (t0 + r) * VT + j0, dor[r]);
+        Row4 x[2] = {}, p[2] = {};
+        rows_times<2>(kq + t0 * LDX, LDX, sm.st + j0, 0, DK, x);                    // K dS'
+        __syncthreads();
+        cols2_times(sm.p + t0, LDW, sm.x + j0, low, 64, p);                         // P^T dO, P lower
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = t0 + r;
+            str(sm.y + t * VT + j0, mul_row(g.bt[t], fma_row(scale, p[r], mul_row(g.eo[t], x[r]))));
         }
         __syncthreads();
-        if (krow) {
+        Row4 e[2] = {};
+        cols2_times(sm.t + t0, LDW, sm.y + j0, low, 64, e);                         // T^T
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = r0 + r;
-                float4 p = ld4(x + t * VT + j0);
-                p.x = scale * p.x + eo[t] * acc[r][0]; p.y = scale * p.y + eo[t] * acc[r][1];
-                p.z = scale * p.z + eo[t] * acc[r][2]; p.w = scale * p.w + eo[t] * acc[r][3];
-                st4(y + t * VT + j0, make_float4(bt[t] * p.x, bt[t] * p.y, bt[t] * p.z, bt[t] * p.w));
+        for (int r = 0; r < 2; ++r) {
+            const int t = t0 + r;
+            if (in) {
+                st4(w.DV + (ch * 64 + t) * DV + col, flat(e[r]));
+                if (t < len) store4(dv + (vrow + t) * DV + col, flat(e[r]));
             }
+            str(sm.z + t * VT + j0, t < len ? mul_row(-g.ea[t], e[r]) : Row4{0, 0});
+            str(sm.x + t * VT + j0, mul_row(scale * g.ea[t], dor[r]));
         }
+        if (c > 0 && tid < 64) gr.put(sm.g[(c - 1) & 1], tid);
         __syncthreads();
-        if (krow) {
-            float e[4][4] = {};
-            for (int i = r0; i < 64; ++i) fma4x4(e, ld4(tm + i * LDT + r0), ld4(y + i * VT + j0));
+        if (c > 0) stage_tp(c - 1);
+        if (4 * u < DK) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = r0 + r;
-                const float4 p = make_float4(e[r][0], e[r][1], e[r][2], e[r][3]);
-                if (in) {
-                    st4(w.DV + (ch * 64 + t) * DV + col, p);
-                    if (t < len) store4(dv + (vrow + t) * DV + col, p);
-                }
-                const float f = t < len ? -ea[t] : 0.f;
-                st4(x + t * VT + j0, make_float4(f * p.x, f * p.y, f * p.z, f * p.w));
-            }
-        } else {
+            for (int r = 0; r < 4; ++r) s[r] = mul_row(g.ea[63], s[r]);
+            cols4_times(kq + 4 * u, LDX, sm.z + j0, s);
+            cols4_times(kq + 64 * LDX + 4 * u, LDX, sm.x + j0, s);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {   // dO is no longer read
-                const int t = r0 - 64 + r;
-                float4 p = ld4(dob + t * VT + j0);
-                const float f = scale * ea[t];
-                st4(dob + t * VT + j0, make_float4(f * p.x, f * p.y, f * p.z, f * p.w));
-            }
-        }
-        __syncthreads();
-        if (r0 < DK) {
-            float s[4][4];
-            const float f = ea[63];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float4 p = ld4(ds + (r0 + r) * VT + j0);
-                s[r][0] = f * p.x; s[r][1] = f * p.y; s[r][2] = f * p.z; s[r][3] = f * p.w;
-            }
-            for (int j = 0; j < 128; j += 4) {
-                const float *z = j < 64 ? x + j * VT + j0 : dob + (j - 64) * VT + j0;   // K with -e^a dV, Q with scale e^a dO
-                float4 kr[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) kr[r] = ld4(kq + (r0 + r) * LDR + j);
-                fma4x4(s, make_float4(kr[0].x, kr[1].x, kr[2].x, kr[3].x), ld4(z));
-                fma4x4(s, make_float4(kr[0].y, kr[1].y, kr[2].y, kr[3].y), ld4(z + VT));
-                fma4x4(s, make_float4(kr[0].z, kr[1].z, kr[2].z, kr[3].z), ld4(z + 2 * VT));
-                fma4x4(s, make_float4(kr[0].w, kr[1].w, kr[2].w, kr[3].w), ld4(z + 3 * VT));
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) st4(ds + (r0 + r) * VT + j0, make_float4(s[r][0], s[r][1], s[r][2], s[r][3]));
+            for (int r = 0; r < 4; ++r) str(sm.st + (4 * u + r) * VT + j0, s[r]);
         }
     }
-    __syncthreads();
     for (int i = tid; i < (S - n) * 8; i += 256) {
         const int j = c0 + (i & 7) * 4;
         if (j < DV) store4(dv + ((size_t)bhv * S + n + (i >> 3)) * DV + j, make_float4(0.f, 0.f, 0.f, 0.f));
     }
-    if (dS0)
-        for (int i = tid; i < DK * 8; i += 256) {
-            const int d = i >> 3, j = (i & 7) * 4;
-            if (c0 + j < DV) st4(dS0 + ((size_t)bhv * DK + d) * DV + c0 + j, ld4(ds + d * VT + j));
-        }
+    if (dS0 && mine) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) st4(dS0 + ((size_t)bhv * DK + 4 * u + r) * DV + col, flat(s[r]));
+    }
 }
 
 // ---------------------------------------------------------------- gradients of a chunk
@@ -667,9 +759,9 @@ cudaError_t prep_t(const Args &a, const Workspace &w, bool kk)
 template <typename T, bool KEEP>
 cudaError_t walk_t(const Args &a, const Workspace &w, void *o, float *S_final)
 {
-    cudaError_t e = smem_limit(walk_kernel<T, KEEP>, WALK_SMEM);
+    cudaError_t e = smem_limit(walk_kernel<T, KEEP>, sizeof(WalkSmem));
     if (e != cudaSuccess) return e;
-    return launch_kernel(walk_kernel<T, KEEP>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(256), WALK_SMEM, a.stream, 1,
+    return launch_kernel(walk_kernel<T, KEEP>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(256), sizeof(WalkSmem), a.stream, 1,
                          (const T *)a.q, (const T *)a.k, (const T *)a.v, a.beta, a.lengths, a.S0, a.NH, a.NHV, a.S,
                          a.DK, a.DV, a.scale, w, (T *)o, S_final);
 }
@@ -677,9 +769,9 @@ cudaError_t walk_t(const Args &a, const Workspace &w, void *o, float *S_final)
 template <typename T>
 cudaError_t reverse_t(const Args &a, const Workspace &w, const void *d_o, const float *dS_final, void *dv, float *dS0)
 {
-    cudaError_t e = smem_limit(reverse_kernel<T>, REV_SMEM);
+    cudaError_t e = smem_limit(reverse_kernel<T>, sizeof(WalkSmem));
     if (e != cudaSuccess) return e;
-    return launch_kernel(reverse_kernel<T>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(256), REV_SMEM, a.stream, 1,
+    return launch_kernel(reverse_kernel<T>, dim3((a.DV + VT - 1) / VT, a.B * a.NHV), dim3(256), sizeof(WalkSmem), a.stream, 1,
                          (const T *)a.q, (const T *)a.k, (const T *)d_o, a.beta, a.lengths, dS_final, a.NH, a.NHV, a.S,
                          a.DK, a.DV, a.scale, w, (T *)dv, dS0);
 }

@@ -14,9 +14,11 @@
 //            dg_t = sum_{i >= t} (Zq . Q + Zk . K)_i + sum_{j < t} (W . K)_j
 //                   + sum_{j < t <= i} (dP * P + dA * KK)_ij + e^{a_64} <S, dS'>
 // (dP * D masked to j <= i, dA * D to j < i.)  Only the walks are sequential over the chunks; their
-// work splits over value columns, 32 to a CTA.  Products are register tiles of 4 x 4 or 8 x 8 fed by
-// 16-byte shared-memory loads with the reduction index outermost; what bounds these kernels is the
-// CUDA cores' fp32 rate and, for few heads, the chain of three products per chunk.
+// work splits over value columns, 32 to a CTA.  Products are register tiles of 2 x 4, 4 x 4 or 8 x 8 fed by
+// 16-byte shared-memory loads, 512 bytes a warp whether lanes read the same or not; at 128 bytes a cycle and SM these
+// bound the walks (8 us a chunk at DK 96, two thirds of it the two products with the state), and the gradients'
+// tiles of 8 x 8 sit where loads and fp32 arithmetic take as long.  For few heads the walks leave SMs idle: their
+// chain of three products per chunk is what a call then waits for.
 #include "gdelta_prep.cuh"
 #include "tc_common.cuh"
 
@@ -131,7 +133,8 @@ prep_kernel(const T *__restrict__ q, const T *__restrict__ k, const float *__res
 // tokens 2 u and 2 u + 1 and the state's rows 4 u .. 4 u + 3, four columns each.  The state stays in registers, with
 // a copy in shared memory for the products that read all of it.  Everything is row-major as it lies in memory, so
 // that the copies are plain and asynchronous: the next chunk's K and Q arrive during the whole of this one, T and P,
-// which have no second buffer, during the state's update.
+// which have no second buffer, during the state's update.  2 x 6 heads of 777 tokens, 96 x 200, take 106 us; with the
+// tiles transposed on their way in by the threads, and half the warps at E, the other half at O, they took 211.
 
 constexpr int LDX = 132;   // row stride of K and Q: rows 2 u .. of a warp's four u start 8 banks apart
 constexpr int LDW = 68;    // of T and P, likewise
@@ -518,7 +521,11 @@ MLSTM_DEVINL float half_warp_sum(float x)
     return x;
 }
 
-// One CTA per chunk and key head, over the value heads on it; dq and dk stay in registers.
+// One CTA per chunk and key head, over the value heads on it; dq and dk stay in registers.  Where that leaves half
+// the SMs without a CTA, one per value head (gridDim.z of them): each then leaves its share of dq and dk in fp32
+// where its states were, which it has read, and sum_heads_kernel adds them in order.  4 key heads of 333 tokens with
+// three value heads each, 64 x 72 (24 CTAs or 72): 61 us, 6 of them the
+// sum, against 147.
 template <typename T>
 __global__ void __launch_bounds__(256, 1)
 grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ d_o,
@@ -537,6 +544,8 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     float *ssum = zout + 64;                      // [32]
     float2 *a = reinterpret_cast<float2 *>(ssum + 32);
     const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
+    const bool split = gridDim.z > 1;
+    const int h0 = split ? blockIdx.z : 0, h1 = split ? h0 + 1 : group;
     const int ty = tid >> 4, tx = tid & 15;
     griddep_wait();
     griddep_launch_dependents();
@@ -545,12 +554,12 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
     const size_t row0 = (size_t)bh * S + c * CH;
     const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
     const int first = max(len, 0);
-    for (int i = tid; i < (full - first) * (DK / 4); i += 256) {   // padding
+    for (int i = tid; h0 == 0 && i < (full - first) * (DK / 4); i += 256) {   // padding
         const size_t at = (row0 + first) * DK + (size_t)i * 4;
         store4(dq + at, zero4);
         store4(dk + at, zero4);
     }
-    for (int h = 0; h < group; ++h)
+    for (int h = h0; h < h1; ++h)
         if (tid < full - first) {
             const size_t gt = (size_t)(b * NHV + (bh % NH) * group + h) * S + c * CH + first + tid;
             dg[gt] = 0.f;
@@ -564,7 +573,7 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         st4(qs + r * LDK + d, ok ? load4(q + (row0 + r) * DK + d) : zero4);
     }
     float acc[8][8] = {};   // rows 4 ty + {0..3} of dq, and of dk
-    for (int h = 0; h < group; ++h) {
+    for (int h = h0; h < h1; ++h) {
         const int bhv = b * NHV + (bh % NH) * group + h;
         const size_t ch = (size_t)bhv * w.NC + c, vrow = (size_t)bhv * S + c * CH;
         __syncthreads();
@@ -726,10 +735,40 @@ grad_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         for (int s = 0; s < 2; ++s) {
             const int d = 64 * s + 4 * tx;
             if (d >= DK) continue;
+            if (split) {
+                const size_t at = ((size_t)(b * NHV + (bh % NH) * group + h0) * w.NC + c) * DK * DV + (size_t)t * DK + d;
+                st4(w.SC + at, make_float4(acc[r][4 * s], acc[r][4 * s + 1], acc[r][4 * s + 2], acc[r][4 * s + 3]));
+                st4(w.DSC + at, make_float4(acc[4 + r][4 * s], acc[4 + r][4 * s + 1], acc[4 + r][4 * s + 2], acc[4 + r][4 * s + 3]));
+                continue;
+            }
             store4(dq + (row0 + t) * DK + d, make_float4(acc[r][4 * s], acc[r][4 * s + 1], acc[r][4 * s + 2], acc[r][4 * s + 3]));
             store4(dk + (row0 + t) * DK + d,
                    make_float4(acc[4 + r][4 * s], acc[4 + r][4 * s + 1], acc[4 + r][4 * s + 2], acc[4 + r][4 * s + 3]));
         }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+sum_heads_kernel(const int *__restrict__ lengths, int NH, int NHV, int S, int DK, int DV, Workspace w, T *__restrict__ dq,
+                 T *__restrict__ dk)
+{
+    const int c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int len = min(CH, live_tokens(lengths, b, S) - c * CH);
+    const size_t first = (size_t)(b * NHV + (bh % NH) * group) * w.NC + c, step = (size_t)w.NC * DK * DV;
+    for (int i = threadIdx.x; i < len * (DK / 4); i += 256) {
+        const float *x = w.SC + first * DK * DV + (size_t)i * 4, *y = w.DSC + first * DK * DV + (size_t)i * 4;
+        float4 q4 = ld4(x), k4 = ld4(y);
+        for (int h = 1; h < group; ++h) {
+            const float4 a = ld4(x + h * step), e = ld4(y + h * step);
+            q4 = make_float4(q4.x + a.x, q4.y + a.y, q4.z + a.z, q4.w + a.w);
+            k4 = make_float4(k4.x + e.x, k4.y + e.y, k4.z + e.z, k4.w + e.w);
+        }
+        const size_t at = ((size_t)bh * S + c * CH) * DK + (size_t)i * 4;
+        store4(dq + at, q4);
+        store4(dk + at, k4);
     }
 }
 
@@ -781,9 +820,14 @@ cudaError_t grad_t(const Args &a, const Workspace &w, const void *d_o, void *dq,
 {
     cudaError_t e = smem_limit(grad_kernel<T>, GRAD_SMEM);
     if (e != cudaSuccess) return e;
-    return launch_kernel(grad_kernel<T>, dim3(w.NC, a.B * a.NH), dim3(256), GRAD_SMEM, a.stream, 1, (const T *)a.q,
-                         (const T *)a.k, (const T *)d_o, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.DV, a.scale, w,
-                         (T *)dq, (T *)dk, dg, dbeta);
+    // the shares take 64 rows of DK where DK rows of DV were
+    const bool split = a.NHV > a.NH && a.DV >= 64 && 2ll * w.NC * a.B * a.NH <= 148;
+    e = launch_kernel(grad_kernel<T>, dim3(w.NC, a.B * a.NH, split ? a.NHV / a.NH : 1), dim3(256), GRAD_SMEM, a.stream, 1,
+                      (const T *)a.q, (const T *)a.k, (const T *)d_o, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.DV,
+                      a.scale, w, (T *)dq, (T *)dk, dg, dbeta);
+    if (e != cudaSuccess || !split) return e;
+    return launch_kernel(sum_heads_kernel<T>, dim3(w.NC, a.B * a.NH), dim3(256), 0, a.stream, 1, a.lengths, a.NH, a.NHV,
+                         a.S, a.DK, a.DV, w, (T *)dq, (T *)dk);
 }
 
 }  // namespace

@@ -168,6 +168,7 @@ MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync
 // The inverse (diagonal blocks of 16 by substitution,
 // then joins, as invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
 // tiles fed by two 16-byte loads per reduction step; four CTAs an SM overlap their short serial parts.
+template <bool BACKWARD>
 __global__ void __launch_bounds__(prep::THREADS, 4)
 prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const float *__restrict__ g, const float *__restrict__ beta, const int *__restrict__ lengths, int NH,
@@ -232,7 +233,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const float b0 = 2 * lane < len ? beta[gt + 2 * lane] : 0.f;
                 const float b1 = 2 * lane + 1 < len ? beta[gt + 2 * lane + 1] : 0.f;
                 chunk_gates_log2(g + gt, len, lane, a0, a1);
-                if (w.A) {
+                if (BACKWARD) {
                     w.A[ch * 64 + 2 * lane] = a0;
                     w.A[ch * 64 + 2 * lane + 1] = a1;
                 }
@@ -273,7 +274,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                     for (int s = 0; s < 16; ++s) x[s] = 0.f;
                 }
-                if (w.KK) {   // the backward's KK and P
+                if (BACKWARD) {   // its KK and P
                     float *dst = (krow ? w.KK : w.P) + ch * 4096 + i * 64 + half * 16;
 #pragma unroll
                     for (int s = 0; s < 16; s += 4)
@@ -346,7 +347,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
                     *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
-                    if (w.TL && part == 0) {   // the backward's third part of T - I
+                    if (BACKWARD && part == 0) {   // the backward's third part of T - I
                         float z[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -802,9 +803,10 @@ bool make_maps(const Args &a, Maps *m)
 
 cudaError_t launch_prep_tc(const Args &a, const Workspace &w, const Maps &m)
 {
-    const cudaError_t e = ensure_dynamic_smem((const void *)prep_tc_kernel, prep::TOTAL);
+    auto kernel = w.KK ? prep_tc_kernel<true> : prep_tc_kernel<false>;
+    const cudaError_t e = ensure_dynamic_smem((const void *)kernel, prep::TOTAL);
     if (e != cudaSuccess) return e;
-    return launch_kernel(prep_tc_kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, m.q, m.k,
+    return launch_kernel(kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, m.q, m.k,
                          a.g, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.scale, w);
 }
 

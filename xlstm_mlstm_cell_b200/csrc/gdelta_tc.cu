@@ -385,21 +385,22 @@ struct Walk {
     static constexpr int EPI = 4 * (CW / 16);              // epilogue warps per chain, 16 columns each
     static constexpr int THREADS = 64 + 32 * NCH * EPI;
     static constexpr int STAGES = 2;
-    // [K; Q] 32 KB, [T - I; G] values and residues 16 KB each.  KEEP has no use for Q and G, whose lanes' sums stay
-    // unread: K alone, with Q's place left as it is, and three parts of T - I, 8 KB each
-    static constexpr uint32_t STAGE = MODE == KEEP ? 57344 : 65536;
-    static constexpr uint32_t LOADED = MODE == KEEP ? 40960 : 65536;
+    // A stage: [K; Q] as two blocks of 64 columns, then [T - I; G] values and residues, 16 KB each.  KEEP has no use
+    // for Q and G, whose lanes' sums stay unread: K alone, and three parts of T - I, 8 KB each; the MMAs' rows 64..127
+    // are then whatever follows.
+    static constexpr uint32_t KROWS = MODE == KEEP ? 64 : 128, KB = KROWS * 128, TOFF = 2 * KB;
+    static constexpr uint32_t STAGE = TOFF + (MODE == KEEP ? 24576 : 32768);
     static constexpr uint32_t BLOCKS = (3 * CW + 63) / 64; // blocks of 64 columns that hold an operand's parts
     static constexpr uint32_t SP = STAGES * STAGE;         // per chain: S parts, 128 rows
     static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
     static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : 64;   // (reverse: K's tokens, then Q's)
     static constexpr uint32_t DO = YN + NCH * BLOCKS * YROWS * 128; // reverse: dO, 64 rows, the chains side by side
-    // the backward: an epilogue warp's 32 rows of fp32 results on their way out, 2 KB each: states of every warp,
-    // tokens' rows of the K tokens' warps
-    static constexpr uint32_t OS = DO + (MODE == REVERSE ? 8192 : 0), OT = OS + (MODE == FORWARD ? 0 : NCH * EPI * 2048);
-    static constexpr uint32_t BAR = OT + (MODE == FORWARD ? 0 : NCH * EPI * 1024);
+    // the backward: an epilogue warp's 32 rows of fp32 results on their way out
+    static constexpr uint32_t OUT = DO + (MODE == REVERSE ? 8192 : 0);
+    static constexpr uint32_t BAR = OUT + (MODE == FORWARD ? 0 : NCH * EPI * 2048);
     static constexpr uint32_t NBAR = 2 * STAGES + 7 * NCH;
     static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
+    static_assert(TOTAL <= 232448, "one CTA's shared memory");
     // TMEM columns of a chain: X and [E; F], 3 CW each; D over X, or (reverse) beside them with G^T dO
     static constexpr uint32_t TX = 0, TE = 3 * CW, TD = MODE == REVERSE ? 6 * CW : 0, TG = 9 * CW;
     static constexpr uint32_t TCH = MODE == REVERSE ? 10 * CW : 6 * CW;
@@ -478,18 +479,18 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int st = c % NST, ci = MODE == REVERSE ? nc - 1 - c : c;
                 if (c >= NST && !mbar_wait(&empty[st], (uint32_t)(c / NST - 1) & 1u, wc)) break;
                 uint8_t *s = smem + st * W::STAGE;
-                mbar_arrive_expect_tx(&full[st], W::LOADED);
+                mbar_arrive_expect_tx(&full[st], W::STAGE);
                 for (int kb = 0; kb < 2; ++kb) {
-                    tma_load_3d(s + kb * 16384, &tm_k, 64 * kb, ci * CH, bh, &full[st]);
-                    if (MODE != KEEP) tma_load_3d(s + kb * 16384 + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
+                    tma_load_3d(s + kb * W::KB, &tm_k, 64 * kb, ci * CH, bh, &full[st]);
+                    if (MODE != KEEP) tma_load_3d(s + kb * W::KB + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
                 }
                 const size_t ch = (size_t)bhv * p.w.NC + ci;
                 if (MODE == KEEP) {
-                    bulk_load(s + 32768, p.w.TG + ch * 32768, 8192, &full[st]);
-                    bulk_load(s + 40960, p.w.TG + ch * 32768 + 16384, 8192, &full[st]);
-                    bulk_load(s + 49152, p.w.TL + ch * 8192, 8192, &full[st]);
+                    bulk_load(s + W::TOFF, p.w.TG + ch * 32768, 8192, &full[st]);
+                    bulk_load(s + W::TOFF + 8192, p.w.TG + ch * 32768 + 16384, 8192, &full[st]);
+                    bulk_load(s + W::TOFF + 16384, p.w.TL + ch * 8192, 8192, &full[st]);
                 } else {
-                    bulk_load(s + 32768, p.w.TG + ch * 32768, 32768, &full[st]);
+                    bulk_load(s + W::TOFF, p.w.TG + ch * 32768, 32768, &full[st]);
                 }
             }
         }
@@ -503,12 +504,12 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // reverse: T^T and G^T, M = 64; the 64 M behind read what lies behind, into lanes that nothing uses
             constexpr uint32_t IDG0 = idesc_bf16(128, CW, 0, 1), RES = MODE == KEEP ? 512 : 1024;
             constexpr uint32_t IDTM = idesc_bf16(128, 2 * CW, 1, 1), IDG = idesc_bf16(128, CW, 1, 1);
-            const uint64_t atm = smem_desc(smem_u32(smem) + 32768, 8192, 1024);
+            const uint64_t atm = smem_desc(smem_u32(smem) + W::TOFF, 8192, 1024);
             const uint64_t bo = MODE == REVERSE ? smem_desc(smem_u32(smem + W::DO), 8192, 1024) : 0;
             const uint64_t bs = smem_desc(smem_u32(smem + W::SP), 16384, 1024);
             const uint64_t by = smem_desc(smem_u32(smem + W::YN), W::YROWS * 128, 1024);
-            const uint64_t ak = smem_desc(smem_u32(smem), 16, 1024), at = smem_desc(smem_u32(smem) + 32768, 16, 1024);
-            const uint64_t ad = smem_desc(smem_u32(smem), 16384, 1024);
+            const uint64_t ak = smem_desc(smem_u32(smem), 16, 1024), at = smem_desc(smem_u32(smem) + W::TOFF, 16, 1024);
+            const uint64_t ad = smem_desc(smem_u32(smem), W::KB, 1024);
             bool ok = true;
             for (int c = 0; c < nc && ok; ++c) {
                 const int st = c % NST;
@@ -520,7 +521,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < KS; ++k)
-                        mma_ss(tmem + h * W::TCH + W::TX, ak + so + (uint64_t)((k >> 2) * 1024 + (k & 3) * 2),
+                        mma_ss(tmem + h * W::TCH + W::TX, ak + so + (uint64_t)((k >> 2) * (W::KB / 16) + (k & 3) * 2),
                                bs + (uint64_t)(h * BS + k * 128), IDX, k > 0);
                     mma_commit(&x_done[h]);
                 };
@@ -593,8 +594,9 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             s[2 * e] = f2_pack(x.x, x.y);
             s[2 * e + 1] = f2_pack(x.z, x.w);
         }
-        // the warp's 32 rows of 16 fp32 columns to rows r0 .. of chunk ci's array, by way of `buf`
-        auto send = [&](uint8_t *buf, const CUtensorMap &tm, int r0, int ci, const uint64_t (&x)[8]) {
+        // the warp's 32 rows of 16 fp32 columns to rows r0 .. of chunk ci's array, by way of its buffer
+        uint8_t *buf = smem + W::OUT + (warp - 2) * 2048;
+        auto send = [&](const CUtensorMap &tm, int r0, int ci, const uint64_t (&x)[8]) {
             if (live_cols <= 0) return;
             if (lane == 0) bulk_wait_read0();
             __syncwarp();
@@ -616,7 +618,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_ready[h]);
-            if (MODE != FORWARD && quad * 32 < p.DK) send(smem + W::OS + (warp - 2) * 2048, tm_s, quad * 32, ci, s);
+            if (MODE != FORWARD && quad * 32 < p.DK) send(tm_s, quad * 32, ci, s);
             // the token's gates and its row of V (reverse: dO, the rows of Q's warps): asked for here, they
             // arrive while X is computed; a load in flight at one of the fences would hold it up.  The next
             // chunk's row is brought to L2
@@ -703,13 +705,13 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // padding: its keys meet N's zeros, which NaN would survive.  X of the other chain may still
                     // read them (into lanes that nothing uses); its D is issued after this chain's N arrived
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(t, j, W::KROWS)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&n_ready[h]);
-                if (MODE != FORWARD) send(smem + W::OT + (h * W::EPI / 2 + cg * 2 + quad) * 2048, tm_t, quad * 32, ci, x);
+                if (MODE != FORWARD) send(tm_t, quad * 32, ci, x);
             }
             if (MODE == FORWARD ? !krow && t < len : MODE == REVERSE && krow && t < len) {
                 __nv_bfloat16 *o = p.o + ((size_t)bhv * p.S + ci * CH + t) * p.DV + col;
@@ -782,10 +784,10 @@ cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const Maps &qk, co
                             !tcfwd::make_map_f32(&m[3], MODE == KEEP ? w.E : w.DV, a.DV, 64, a.B * a.NHV * w.NC)))
         return cudaErrorUnknown;
     // While the GPU has SMs for it a CTA takes 32 columns; 64 take fewer CTAs than twice the time (the epilogue
-    // warps of the K tokens, two of the SM's four schedulers, are what a chunk then waits for).  The backward's
-    // walks always take 32: their results' way out takes the shared memory
-    const bool narrow = MODE != FORWARD || (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
-    if constexpr (MODE == FORWARD)
+    // warps of the K tokens, two of the SM's four schedulers, are what a chunk then waits for).  The reverse
+    // walk always takes 32: Q's share of the update and the results' way out take the shared memory
+    const bool narrow = MODE == REVERSE || (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
+    if constexpr (MODE != REVERSE)
         if (!narrow) return a.DK > 64 ? launch_walk_cw<32, 8, MODE>(a, w, m, v, S0, o, S_final)
                                       : launch_walk_cw<32, 4, MODE>(a, w, m, v, S0, o, S_final);
     return a.DK > 64 ? launch_walk_cw<16, 8, MODE>(a, w, m, v, S0, o, S_final)

@@ -168,6 +168,10 @@ MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync
 // The inverse (diagonal blocks of 16 by substitution,
 // then joins, as invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
 // tiles fed by two 16-byte loads per reduction step; four CTAs an SM overlap their short serial parts.
+// 8192 chunks of 128 key elements in pairs of value heads take 224 us, 1.5 us a chunk's SM: half of the
+// shared-memory rate, the rest barriers between the joins.  G on the tensor cores needs P and T in three parts each
+// (two lose 1e-4 of beta's gradient where keys repeat) and took 305 us with their splitting; CTAs of 64 threads
+// 222 to 300 us.
 template <bool BACKWARD>
 __global__ void __launch_bounds__(prep::THREADS, 4)
 prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -375,7 +379,11 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 // ---------------------------------------------------------------- walk
 
 // A CTA runs two chains side by side, CW value columns each, on the same K, Q, T and G tiles: while the
-// epilogue warps of one pass over an accumulator, the MMAs of the other run.
+// epilogue warps of one pass over an accumulator, the MMAs of the other run.  What bounds a walk is that chain: 2.1 us
+// a chunk at CW 16 (32 heads of 16384 tokens, 128 x 128: 548 us, 128 CTAs); with the states
+// and E kept 2.6 us, at CW 32 4.6 us (4 x 16 heads of 4096 tokens: 292 us, against 338 in two rounds of CTAs at CW
+// 16); reverse 3.2 us.  The tensor pipe is busy a quarter of it, the rest are the epilogues' passes from TMEM over registers to shared memory and the
+// waits between the two.  One chain of 32 columns, three or four chains, or 8 columns a thread were no faster.
 enum Mode { FORWARD, KEEP, REVERSE };   // KEEP: the forward walk again, for the backward: states and E, no outputs
 
 template <int CW, int MODE>

@@ -10,11 +10,12 @@
 // step) a token's heads are dealt to several groups.  VEC is the widest vector that sizes, strides and
 // pointers allow, at most four elements.
 //
-// What it costs beyond the bytes is instructions and registers: packed fp32 pairs, one side per CTA and
-// four vectors loaded ahead took the forward pass over 16384 tokens of 16 + 16 heads of 128 (bf16, 268 MB)
-// from 106 to 64 us (4.2 TB/s) and the backward of 4 x 4096 tokens of 16 + 4 heads (252 MB) from 133 to
-// 72 us with the weights' sums (3.5 TB/s); two vectors ahead 68 and 73 us, tokens shared by a CTA with the
-// angles in shared memory 74 and 126 us.
+// What it costs beyond the bytes is instructions, registers and bytes in flight.  Packed fp32 pairs, one side per CTA,
+// four vectors on their way at any time (the next is asked for as soon as one is done with) and lanes without a unit
+// that go along instead of branching take the forward pass over 16384 tokens of 16 + 16 heads of 128 (bf16, 268 MB,
+// cold) to 61 us (4.4 TB/s) and the backward of 4 x 4096 tokens of 16 + 4 heads (252 MB) to 71 us with the weights'
+// sums (3.5 TB/s).  Loading four and then working on four took 67 and 77 us, tokens shared by a CTA with the angles in
+// shared memory 74 and 126 us.
 #include "common.cuh"
 #include "qknorm.h"
 #include "tc_common.cuh"
@@ -32,7 +33,19 @@ using namespace tc;   // packed fp32 pairs
 constexpr int THREADS = 128;
 // SPAN: VEC elements times units per lane, 4 for vectors of up to 256 (32 lanes x 2 x 4), 8 beyond.  Wider
 // loads (8 bf16) with half the lanes took twice the registers and were slower for it.
-constexpr int AHEAD = 4;     // vectors a group loads before it works on the first of them
+// Vectors a group loads before it works on the first of them: what 32 registers hold, at most four.
+template <typename T, int VEC, int SPAN, bool BWD>
+constexpr int ahead()
+{
+    constexpr int words = SPAN * 2 / VEC * ((int)sizeof(T) * VEC < 4 ? 1 : (int)sizeof(T) * VEC / 4) * (BWD ? 2 : 1);
+    return words >= 32 ? 1 : words >= 16 ? 2 : 4;
+}
+// CTAs an SM, for the registers that leaves each.
+template <typename T, int VEC, int SPAN, bool BWD>
+constexpr int resident()
+{
+    return SPAN == 8 ? (BWD ? 2 : 3) : BWD ? 4 : sizeof(T) == 2 && VEC == 4 ? 6 : 4;
+}
 
 struct Side {                // queries or keys
     const void *x, *dy;
@@ -171,7 +184,7 @@ MLSTM_DEVINL void rotate(uint64_t (&x)[VEC], const float2 (&cs)[VEC], float sign
 // A group's place: its lane, its token and what it needs of it.
 template <int VEC, int SPAN>
 struct Place {
-    int gl, units, hs;            // units: of a vector, 0 for a group without a token
+    int gl, units, hs;            // units: of a vector
     unsigned b, t;
     float2 cs[SPAN / VEC][VEC];   // of the lane's pairs
 };
@@ -205,114 +218,127 @@ struct Held {
     Vec<T, VEC> x[SPAN / VEC][2], d[BWD ? SPAN / VEC : 1][2];
 };
 
-// All of a token's heads of one side.  gw: the lane's share of the weight's gradient.
+// All of a token's heads of one side.  gw: the lane's share of the weight's gradient.  `on`: the group has a token;
+// a warp's groups stay together for the sums either way.  A lane without a unit goes along with the vector's last one,
+// counts nothing of it and stores nothing: branches around it cost more than its arithmetic.
 template <typename T, int VEC, int SPAN, bool INTER, bool BWD>
-MLSTM_DEVINL void one_side(const Params &p, const Side &sd, const Place<VEC, SPAN> &g, uint64_t *gw)
+MLSTM_DEVINL void one_side(const Params &p, const Side &sd, const Place<VEC, SPAN> &g, bool on, uint64_t *gw)
 {
-    constexpr int NU = SPAN / VEC;
-    const T *x = (const T *)sd.x + g.b * sd.xs.batch + g.t * sd.xs.token;
-    const long long c0 = ((long long)g.b * sd.heads * p.S + g.t) * p.D, ch = (long long)p.S * p.D;   // contiguous tensors
-    const T *dy = (const T *)sd.dy + c0;
-    T *out = (T *)sd.out + (BWD ? g.b * sd.os.batch + g.t * sd.os.token : c0);
-    const long long oh = BWD ? sd.os.head : ch;
+    constexpr int NU = SPAN / VEC, AHEAD = ahead<T, VEC, SPAN, BWD>();
     uint64_t w[NU][VEC];
     bool has[NU];
     int o1[NU], o2[NU];
     bool turn[NU];
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
-        const int u = g.gl + n * p.GL;
-        has[n] = u < g.units;
+        has[n] = g.gl + n * p.GL < g.units;
+        const int u = min(g.gl + n * p.GL, g.units - 1);
         unit_offsets<VEC, INTER>(u, p.D, p.RD, o1[n], o2[n], turn[n]);
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const int f0 = VEC == 1 ? o1[n] : e < VEC / 2 ? o1[n] + 2 * e : o2[n] + 2 * e - VEC;
             const int f1 = VEC == 1 ? o2[n] : f0 + 1;
-            w[n][e] = sd.w && has[n] ? f2_pack(sd.w[f0], sd.w[f1]) : f2_pack(1.f, 1.f);
+            w[n][e] = sd.w ? f2_pack(sd.w[f0], sd.w[f1]) : f2_pack(1.f, 1.f);
         }
     }
+    // one unit: its first element's offset goes into the pointers
+    const int base = NU == 1 ? o1[0] : 0;
+    if (NU == 1) {
+        o2[0] -= base;
+        o1[0] = 0;
+    }
+    const long long c0 = ((long long)g.b * sd.heads * p.S + g.t) * p.D + base, ch = (long long)p.S * p.D;   // contiguous tensors
+    const T *x = (const T *)sd.x + g.b * sd.xs.batch + g.t * sd.xs.token + base + g.hs * sd.xs.head;
+    const T *dy = (const T *)sd.dy + c0 + g.hs * ch;
+    const long long oh = BWD ? sd.os.head : ch;
+    T *out = (T *)sd.out + (BWD ? g.b * sd.os.batch + g.t * sd.os.token + base : c0) + g.hs * oh;
     const float inv_n = p.l2 ? 1.f : 1.f / (float)p.D;
-    const int rounds = (sd.heads + p.HS * AHEAD - 1) / (p.HS * AHEAD);   // the same for every group of the warp
-    int head = g.hs;
-    x += head * sd.xs.head;
-    dy += head * ch;
-    out += head * oh;
     const long long xstep = p.HS * sd.xs.head, cstep = p.HS * ch, ostep = p.HS * oh;
+    using H = Held<T, VEC, SPAN, BWD>;
+    auto load = [&](H &v) {
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            v.x[n][0] = load_vec<T, VEC>(x + o1[n]);
+            v.x[n][1] = load_vec<T, VEC>(x + o2[n]);
+            if (BWD) {
+                v.d[n][0] = load_vec<T, VEC>(dy + o1[n]);
+                v.d[n][1] = load_vec<T, VEC>(dy + o2[n]);
+            }
+        }
+        x += xstep;
+        if (BWD) dy += cstep;
+    };
+    auto work = [&](const H &v, bool live) {
+        uint64_t xv[NU][VEC], d[BWD ? NU : 1][VEC], gwd[BWD ? NU : 1][VEC];   // gwd: d without the weight
+        float s = 0.f, xd = 0.f;
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            uint64_t s2 = 0, xd2 = 0;
+            widen<T, VEC>(v.x[n], xv[n]);
+            if (BWD) {
+                widen<T, VEC>(v.d[n], d[n]);
+                if (turn[n]) rotate<VEC, INTER>(d[n], g.cs[n], -1.f);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                s2 = f2_fma(xv[n][e], xv[n][e], s2);
+                if (BWD) {
+                    gwd[n][e] = d[n][e];
+                    d[n][e] = f2_mul(w[n][e], d[n][e]);
+                    xd2 = f2_fma(d[n][e], xv[n][e], xd2);
+                }
+            }
+            s += has[n] ? f2_unpack(s2).x + f2_unpack(s2).y : 0.f;
+            if (BWD) xd += has[n] ? f2_unpack(xd2).x + f2_unpack(xd2).y : 0.f;
+        }
+        for (int o = p.GL / 2; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (BWD) xd += __shfl_xor_sync(0xffffffffu, xd, o);
+        }
+        const float r = rsqrtf(fmaf(s, inv_n, p.eps));
+        const float back = BWD ? -r * r * r * (xd * inv_n) : 0.f;
+        const uint64_t r2 = f2_pack(r, r), back2 = f2_pack(back, back);
+#pragma unroll
+        for (int n = 0; n < NU; ++n) {
+            if (!has[n] || !live) continue;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                if (BWD) {
+                    gw[n * VEC + e] = f2_fma(gwd[n][e], f2_mul(r2, xv[n][e]), gw[n * VEC + e]);
+                    xv[n][e] = f2_fma(r2, d[n][e], f2_mul(back2, xv[n][e]));
+                } else {
+                    xv[n][e] = f2_mul(xv[n][e], f2_mul(r2, w[n][e]));
+                }
+            }
+            if (!BWD && turn[n]) rotate<VEC, INTER>(xv[n], g.cs[n], 1.f);
+            Vec<T, VEC> y[2];
+            narrow<T, VEC>(xv[n], y);
+            store_vec<T, VEC>(out + o1[n], y[0]);
+            store_vec<T, VEC>(out + o2[n], y[1]);
+        }
+        out += ostep;
+    };
+    // the next vectors are asked for as soon as one is done with: a group always waits for the oldest of AHEAD
+    const int rounds = (sd.heads + p.HS * AHEAD - 1) / (p.HS * AHEAD);   // the same for every group of the warp
+    int left = on ? (sd.heads - g.hs + p.HS - 1) / p.HS : 0;
+    H v[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (k < left) load(v[k]);
 #pragma unroll 1
     for (int round = 0; round < rounds; ++round) {
-        Held<T, VEC, SPAN, BWD> v[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
-#pragma unroll
-            for (int n = 0; n < NU; ++n)
-                if (has[n] && head + k * p.HS < sd.heads) {
-                    v[k].x[n][0] = load_vec<T, VEC>(x + o1[n]);
-                    v[k].x[n][1] = load_vec<T, VEC>(x + o2[n]);
-                    if (BWD) {
-                        v[k].d[n][0] = load_vec<T, VEC>(dy + o1[n]);
-                        v[k].d[n][1] = load_vec<T, VEC>(dy + o2[n]);
-                    }
-                }
-            x += xstep;
-            if (BWD) dy += cstep;
+            work(v[k], k < left);
+            if (k + AHEAD < left) load(v[k]);
         }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const bool on = head < sd.heads;
-            uint64_t xv[NU][VEC], d[BWD ? NU : 1][VEC], gwd[BWD ? NU : 1][VEC], s2 = 0, xd2 = 0;   // gwd: d without the weight
-#pragma unroll
-            for (int n = 0; n < NU; ++n) {
-                if (!has[n] || !on) continue;
-                widen<T, VEC>(v[k].x[n], xv[n]);
-                if (BWD) {
-                    widen<T, VEC>(v[k].d[n], d[n]);
-                    if (turn[n]) rotate<VEC, INTER>(d[n], g.cs[n], -1.f);
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    s2 = f2_fma(xv[n][e], xv[n][e], s2);
-                    if (BWD) {
-                        gwd[n][e] = d[n][e];
-                        d[n][e] = f2_mul(w[n][e], d[n][e]);
-                        xd2 = f2_fma(d[n][e], xv[n][e], xd2);
-                    }
-                }
-            }
-            float s = f2_unpack(s2).x + f2_unpack(s2).y, xd = f2_unpack(xd2).x + f2_unpack(xd2).y;
-            for (int o = p.GL / 2; o > 0; o >>= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (BWD) xd += __shfl_xor_sync(0xffffffffu, xd, o);
-            }
-            const float r = rsqrtf(fmaf(s, inv_n, p.eps));
-            const float back = BWD ? -r * r * r * (xd * inv_n) : 0.f;
-            const uint64_t r2 = f2_pack(r, r), back2 = f2_pack(back, back);
-#pragma unroll
-            for (int n = 0; n < NU; ++n) {
-                if (!has[n] || !on) continue;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    if (BWD) {
-                        gw[n * VEC + e] = f2_fma(gwd[n][e], f2_mul(r2, xv[n][e]), gw[n * VEC + e]);
-                        xv[n][e] = f2_fma(r2, d[n][e], f2_mul(back2, xv[n][e]));
-                    } else {
-                        xv[n][e] = f2_mul(xv[n][e], f2_mul(r2, w[n][e]));
-                    }
-                }
-                if (!BWD && turn[n]) rotate<VEC, INTER>(xv[n], g.cs[n], 1.f);
-                Vec<T, VEC> y[2];
-                narrow<T, VEC>(xv[n], y);
-                store_vec<T, VEC>(out + o1[n], y[0]);
-                store_vec<T, VEC>(out + o2[n], y[1]);
-            }
-            head += p.HS;
-            out += ostep;
-        }
+        left -= AHEAD;
     }
 }
 
 // blockIdx.y: queries or keys.
 template <typename T, int VEC, int SPAN, bool INTER, bool BWD>
-__global__ void __launch_bounds__(THREADS, BWD ? 4 : 6)
+__global__ void __launch_bounds__(THREADS, (resident<T, VEC, SPAN, BWD>()))
 qknorm_kernel(const __grid_constant__ Params p)
 {
     extern __shared__ __align__(16) float red[];   // backward: [groups][D]
@@ -324,18 +350,18 @@ qknorm_kernel(const __grid_constant__ Params p)
     griddep_launch_dependents();
     uint64_t gw[BWD ? SPAN : 1] = {};
     const unsigned long long items = (unsigned long long)p.tokens * p.HS, step = (unsigned long long)gridDim.x * groups;
-    // whole warps stay together for the sums: a group without an item goes along without a unit
+    // whole warps stay together for the sums: a group without an item goes along
 #pragma unroll 1
     for (unsigned long long i0 = (unsigned long long)blockIdx.x * groups; i0 < items; i0 += step) {
         const unsigned long long i = i0 + grp;
         const bool on = i < items;
         const unsigned tok = on ? (unsigned)(p.HS == 1 ? i : i / p.HS) : 0u;
-        g.units = on ? p.D / 2 / VEC : 0;
+        g.units = p.D / 2 / VEC;
         g.hs = on && p.HS > 1 ? (int)(i - (unsigned long long)tok * p.HS) : 0;
         g.b = tok / (unsigned)p.S;
         g.t = tok - g.b * (unsigned)p.S;
         if (p.RD) angles<VEC, SPAN, INTER>(p, tok, g);
-        one_side<T, VEC, SPAN, INTER, BWD>(p, sd, g, gw);
+        one_side<T, VEC, SPAN, INTER, BWD>(p, sd, g, on, gw);
     }
     if (BWD && p.part) {   // the groups' shares of the weight's gradient, added in order
         const int units = p.D / 2 / VEC;
@@ -411,7 +437,7 @@ cudaError_t launch(Params p, int *ctas, cudaStream_t stream)
 {
     const int units = p.D / 2 / VEC, heads = std::max(p.side[0].heads, p.side[1].heads);
     p.GL = 1;
-    while (p.GL < 32 && p.GL < units) p.GL *= 2;
+    while (p.GL < 32 && p.GL * (SPAN / VEC) < units) p.GL *= 2;
     const int groups = THREADS / p.GL;
     // a token's heads go to as many groups as it takes to fill the GPU's threads once
     p.HS = (int)std::min<long long>(heads, std::max<long long>(1, 148ll * 1024 / p.GL / p.tokens));

@@ -378,8 +378,8 @@ walk_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restric
         }
     }
     if (KEEP) return;
-    for (int i = tid; i < (S - n) * 8; i += 256) {   // padding
-        const int j = c0 + (i & 7) * 4;
+    for (long long i = tid; i < (S - n) * 8ll; i += 256) {   // padding
+        const int j = c0 + (int)(i & 7) * 4;
         if (j < DV) store4(o + ((size_t)bhv * S + n + (i >> 3)) * DV + j, make_float4(0.f, 0.f, 0.f, 0.f));
     }
     if (S_final && mine) {
@@ -486,8 +486,8 @@ reverse_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__rest
             for (int r = 0; r < 4; ++r) str(sm.st + (4 * u + r) * VT + j0, s[r]);
         }
     }
-    for (int i = tid; i < (S - n) * 8; i += 256) {
-        const int j = c0 + (i & 7) * 4;
+    for (long long i = tid; i < (S - n) * 8ll; i += 256) {
+        const int j = c0 + (int)(i & 7) * 4;
         if (j < DV) store4(dv + ((size_t)bhv * S + n + (i >> 3)) * DV + j, make_float4(0.f, 0.f, 0.f, 0.f));
     }
     if (dS0 && mine) {

@@ -18,7 +18,7 @@
 // reads A once for all three, and the epilogue adds the parts' columns.  T - I and G enter as two parts,
 // value and rounding residue (rms error 2.7e-6 of the correction they carry), T - I in the backward's forward
 // walk as three: dg and dbeta are fp32 outputs, and two parts alone put 4e-7 (DK 128) to 7e-7 (DK 64) into dg
-// through E, against 1e-7 through dV.  K, Q, dO are exact.  Without its unit diagonal T leaves Y itself out of the
+// through E, against 1e-7 through dV; G likewise where DK is at most 64.  K, Q, dO are exact.  Without its unit diagonal T leaves Y itself out of the
 // MMA: the threads that formed Y in fp32 add it to the result.  The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
 // each, and takes the update with fp32 additions.
 //
@@ -351,7 +351,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
                     *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
-                    if (BACKWARD && part == 0) {   // the backward's third part of T - I
+                    if (BACKWARD && (part == 0 || w.GL)) {   // the backward's third part of T - I, and of G where there is room
                         float z[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -359,7 +359,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             z[e] = (y[e] - __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16)) -
                                    __uint_as_float(e & 1 ? l & 0xffff0000u : l << 16);
                         }
-                        *reinterpret_cast<uint2 *>(w.TL + ch * 8192 + sw128_offset(i0 + r, c0, 64)) =
+                        *reinterpret_cast<uint2 *>((part ? w.GL : w.TL) + ch * 8192 + sw128_offset(i0 + r, c0, 64)) =
                             make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
                     }
                 }
@@ -386,18 +386,20 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 // waits between the two.  One chain of 32 columns, three or four chains, or 8 columns a thread were no faster.
 enum Mode { FORWARD, KEEP, REVERSE };   // KEEP: the forward walk again, for the backward: states and E, no outputs
 
-template <int CW, int MODE>
+template <int CW, int KS, int MODE>
 struct Walk {
     static constexpr int NCH = 2;                          // chains
     static constexpr int VT = NCH * CW;                    // value columns of the CTA
     static constexpr int EPI = 4 * (CW / 16);              // epilogue warps per chain, 16 columns each
     static constexpr int THREADS = 64 + 32 * NCH * EPI;
     static constexpr int STAGES = 2;
-    // A stage: [K; Q] as two blocks of 64 columns, then [T - I; G] values and residues, 16 KB each.  KEEP has no use
-    // for Q and G, whose lanes' sums stay unread: K alone, and three parts of T - I, 8 KB each; the MMAs' rows 64..127
-    // are then whatever follows.
-    static constexpr uint32_t KROWS = MODE == KEEP ? 64 : 128, KB = KROWS * 128, TOFF = 2 * KB;
-    static constexpr uint32_t STAGE = TOFF + (MODE == KEEP ? 24576 : 32768);
+    // A stage: [K; Q] as one or two blocks of 64 columns, then [T - I; G] values and residues, 16 KB each.  KEEP has
+    // no use for Q and G, whose lanes' sums stay unread: K alone, and three parts of T - I, 8 KB each; the MMAs' rows
+    // 64..127 are then whatever follows, and so are the state's rows from 64 on with one block.  Reverse, a stage of
+    // one block has room for G's third part.
+    static constexpr uint32_t KROWS = MODE == KEEP ? 64 : 128, KB = KROWS * 128, KBLK = KS / 4, TOFF = KBLK * KB;
+    static constexpr bool G3 = MODE == REVERSE && KS == 4;
+    static constexpr uint32_t STAGE = TOFF + (MODE == KEEP ? 24576 : 32768) + (G3 ? 8192 : 0);
     static constexpr uint32_t BLOCKS = (3 * CW + 63) / 64; // blocks of 64 columns that hold an operand's parts
     static constexpr uint32_t SP = STAGES * STAGE;         // per chain: S parts, 128 rows
     static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
@@ -427,11 +429,11 @@ struct WalkParams {
 };
 
 template <int CW, int KS, int MODE>
-__global__ void __launch_bounds__(Walk<CW, MODE>::THREADS, 1)
+__global__ void __launch_bounds__(Walk<CW, KS, MODE>::THREADS, 1)
 walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_t, const WalkParams p)
 {
-    using W = Walk<CW, MODE>;
+    using W = Walk<CW, KS, MODE>;
     static_assert(MODE != REVERSE || CW == 16, "dO of both chains in one block of columns");
     constexpr int NST = W::STAGES, NCH = W::NCH;
     extern __shared__ uint8_t smem_raw[];
@@ -488,7 +490,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (c >= NST && !mbar_wait(&empty[st], (uint32_t)(c / NST - 1) & 1u, wc)) break;
                 uint8_t *s = smem + st * W::STAGE;
                 mbar_arrive_expect_tx(&full[st], W::STAGE);
-                for (int kb = 0; kb < 2; ++kb) {
+                for (int kb = 0; kb < (int)W::KBLK; ++kb) {
                     tma_load_3d(s + kb * W::KB, &tm_k, 64 * kb, ci * CH, bh, &full[st]);
                     if (MODE != KEEP) tma_load_3d(s + kb * W::KB + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
                 }
@@ -499,6 +501,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     bulk_load(s + W::TOFF + 16384, p.w.TL + ch * 8192, 8192, &full[st]);
                 } else {
                     bulk_load(s + W::TOFF, p.w.TG + ch * 32768, 32768, &full[st]);
+                    if (W::G3) bulk_load(s + W::TOFF + 32768, p.w.GL + ch * 8192, 8192, &full[st]);
                 }
             }
         }
@@ -537,10 +540,16 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 auto issue_q = [&](int h) {
                     if (!(ok = ok && mbar_wait(&o_ready[h], ph, wc))) return;
                     tc_fence_after();
+                    if (W::G3) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_ss(tmem + h * W::TCH + W::TG, atm + so + (uint64_t)(2048 + k * 128),
+                                   bo + (uint64_t)(h * CW / 8 + k * 128), IDG, k > 0);
+                    }
 #pragma unroll
                     for (int k = 7; k >= 0; --k)   // G's rows lie 8 KB into the values' tile, and 16 KB further its residues'
                         mma_ss(tmem + h * W::TCH + W::TG, atm + so + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
-                               bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, k < 7);
+                               bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, W::G3 || k < 7);
 #pragma unroll
                     for (int k = 4; k < 8; ++k)
                         mma_ss(tmem + h * W::TCH + W::TD, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 4);
@@ -656,7 +665,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (!mbar_wait(&full[c % NST], (uint32_t)(c / NST) & 1u, wc)) break;
                     if (h == 0 && cg == 0 && t >= len) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
+                        for (int j = 0; j < 2 * KS; ++j)
                             *reinterpret_cast<uint4 *>(smem + (c % NST) * W::STAGE + sw128_chunk(64 + t, j, 128)) = make_uint4(0u, 0u, 0u, 0u);
                     }
                 }
@@ -713,7 +722,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     // padding: its keys meet N's zeros, which NaN would survive.  X of the other chain may still
                     // read them (into lanes that nothing uses); its D is issued after this chain's N arrived
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(t, j, W::KROWS)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int j = 0; j < 2 * KS; ++j) *reinterpret_cast<uint4 *>(kq + sw128_chunk(t, j, W::KROWS)) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async();
                 tc_fence_before();
@@ -774,7 +783,7 @@ template <int CW, int KS, int MODE>
 cudaError_t launch_walk_cw(const Args &a, const Workspace &w, const CUtensorMap (&m)[4], const void *v, const float *S0,
                            void *o, float *S_final)
 {
-    using W = Walk<CW, MODE>;
+    using W = Walk<CW, KS, MODE>;
     cudaError_t e = ensure_dynamic_smem((const void *)walk_tc_kernel<CW, KS, MODE>, W::TOTAL);
     if (e != cudaSuccess) return e;
     WalkParams p = {static_cast<const __nv_bfloat16 *>(v), S0, a.lengths, static_cast<__nv_bfloat16 *>(o), S_final, a.NH,

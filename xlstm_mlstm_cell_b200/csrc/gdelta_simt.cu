@@ -67,7 +67,9 @@ MLSTM_DEVINL void fma4x4(float (&acc)[4][4], float4 a, float4 b)
 
 constexpr size_t PREP_SMEM = sizeof(float) * (128 * LDR + 64 * LDT + 32 * 33 + 64) + sizeof(float2) * 64;
 
-// One CTA per chunk and key head: K K^T and Q K^T once, then the matrices of every value head on it.
+// One CTA per chunk and key head: K K^T and Q K^T once, then the matrices of every value head on it.  Where all of
+// them find room at once, one per value head instead (gridDim.z of them): 24 CTAs of three heads took
+// 25 us, 72 of one 14.
 template <typename T>
 __global__ void __launch_bounds__(256, 2)
 prep_kernel(const T *__restrict__ q, const T *__restrict__ k, const float *__restrict__ g,
@@ -83,7 +85,7 @@ prep_kernel(const T *__restrict__ q, const T *__restrict__ k, const float *__res
     const int tid = threadIdx.x, c = blockIdx.x, bh = blockIdx.y, b = bh / NH, group = NHV / NH;
     griddep_wait();
     griddep_launch_dependents();
-    if (c == 0 && bh == 0 && tid == 0) *w.status = 0u;
+    if (c == 0 && bh == 0 && blockIdx.z == 0 && tid == 0) *w.status = 0u;
     const int len = min(CH, live_tokens(lengths, b, S) - c * CH);
     if (len <= 0) return;
     const size_t row0 = (size_t)bh * S + c * CH;
@@ -97,7 +99,8 @@ prep_kernel(const T *__restrict__ q, const T *__restrict__ k, const float *__res
         fma4x4(kk, ld4(kq + d * LDR + i0), y);
         fma4x4(qk, ld4(kq + d * LDR + 64 + i0), y);
     }
-    for (int h = 0; h < group; ++h) {
+    const int h0 = gridDim.z > 1 ? blockIdx.z : 0, h1 = gridDim.z > 1 ? h0 + 1 : group;
+    for (int h = h0; h < h1; ++h) {
         const int bhv = b * NHV + (bh % NH) * group + h;
         const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
         __syncthreads();
@@ -791,7 +794,8 @@ cudaError_t prep_t(const Args &a, const Workspace &w, bool kk)
 {
     cudaError_t e = smem_limit(prep_kernel<T>, PREP_SMEM);
     if (e != cudaSuccess) return e;
-    return launch_kernel(prep_kernel<T>, dim3(w.NC, a.B * a.NH), dim3(256), PREP_SMEM, a.stream, 1, (const T *)a.q,
+    const bool split = (long long)w.NC * a.B * a.NHV <= 2 * 148;
+    return launch_kernel(prep_kernel<T>, dim3(w.NC, a.B * a.NH, split ? a.NHV / a.NH : 1), dim3(256), PREP_SMEM, a.stream, 1, (const T *)a.q,
                          (const T *)a.k, a.g, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, w, kk);
 }
 

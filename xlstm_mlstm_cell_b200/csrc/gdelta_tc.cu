@@ -164,7 +164,9 @@ MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync
 }
 }  // namespace prep
 
-// One CTA per chunk and key head: [K; Q] K^T once in TMEM, then the matrices of every value head on it.
+// One CTA per chunk and key head: [K; Q] K^T once in TMEM, then the matrices of every value head on it.  Where all of
+// them find room at once, one per value head instead (gridDim.z of them): 32 CTAs of two heads took 23 us, 64
+// of one 13.
 // The inverse (diagonal blocks of 16 by substitution,
 // then joins, as invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
 // tiles fed by two 16-byte loads per reduction step; four CTAs an SM overlap their short serial parts.
@@ -206,7 +208,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
     griddep_launch_dependents();
-    if (c == 0 && bh == 0 && tid == 0) *w.status = 0u;
+    if (c == 0 && bh == 0 && blockIdx.z == 0 && tid == 0) *w.status = 0u;
     const int len = min(CH, live_tokens(lengths, b, S) - c * CH);
     if (len > 0) {
         if (tid == 0) {
@@ -229,7 +231,8 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         bool ok = true;
         const int i = tid & 63;   // the thread's row: of K K^T in warps 0 and 1, of Q K^T in 2 and 3
         const bool krow = tid < 64;
-        for (int h = 0; h < group; ++h) {
+        const int h0 = gridDim.z > 1 ? blockIdx.z : 0, h1 = gridDim.z > 1 ? h0 + 1 : group;
+        for (int h = h0; h < h1; ++h) {
             const int bhv = b * NHV + (bh % NH) * group + h;
             const size_t ch = (size_t)bhv * w.NC + c, gt = (size_t)bhv * S + c * CH;
             if (warp == 0) {
@@ -245,7 +248,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 ga[2 * lane + 1] = make_float4(a1.x, a1.y, b1, 0.f);
             }
             __syncthreads();
-            if (h == 0) {
+            if (h == h0) {
                 ok = mbar_wait(&bars[1], 0, wc);
                 tc_fence_after();
             }
@@ -825,7 +828,8 @@ cudaError_t launch_prep_tc(const Args &a, const Workspace &w, const Maps &m)
     auto kernel = w.KK ? prep_tc_kernel<true> : prep_tc_kernel<false>;
     const cudaError_t e = ensure_dynamic_smem((const void *)kernel, prep::TOTAL);
     if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, dim3(w.NC, a.B * a.NH), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, m.q, m.k,
+    const bool split = (long long)w.NC * a.B * a.NHV <= 4 * 148;
+    return launch_kernel(kernel, dim3(w.NC, a.B * a.NH, split ? a.NHV / a.NH : 1), dim3(prep::THREADS), prep::TOTAL, a.stream, 1, m.q, m.k,
                          a.g, a.beta, a.lengths, a.NH, a.NHV, a.S, a.DK, a.scale, w);
 }
 

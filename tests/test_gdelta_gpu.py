@@ -418,3 +418,19 @@ def test_step_of_more_heads_than_a_grid_axis_holds(dt):
     ro, rS = oracle.gdelta_fwd(*args(x), state=x["S0"])
     assert_close("o", o, ro[:, :, 0], tol(o))
     assert_close("state", S, rS, F32)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_groups_of_heads_in_one_cta(dt):
+    """More chunks than the GPU holds CTAs for: a key head's value heads share one, in preparation and gradients."""
+    x = make(40, 1, 3, 130, 16, 72, dt, seed=67, rate=0.3)
+    lengths = torch.randint(0, 131, (40,), generator=torch.Generator().manual_seed(68), dtype=torch.int32).cuda()
+    check_fwd(x, state=True, lengths=lengths)
+    check_bwd(x, state=True, dstate=True, lengths=lengths)
+
+
+@pytest.mark.parametrize("DV", [48, 136])
+def test_tensor_cores_with_groups_in_one_cta(DV):
+    x = make(70, 1, 3, 200, 72, DV, "bf16", seed=69, rate=0.3)
+    check_fwd(x, state=True)
+    check_bwd(x, state=True, dstate=True)

@@ -1,0 +1,103 @@
+"""Whose memory the binding allocates from when a call is given a stream (no GPU: the library and CUDA's streams
+are stand-ins that note what happens).
+
+A call's kernels on a given stream do not wait for the current one.  A tensor allocated on the current stream may
+be a block that work queued there still uses; so what a call allocates has to come from the given stream's memory,
+and an output has to be recorded on the current stream, where the caller uses it, before its block can go elsewhere.
+"""
+from __future__ import annotations
+
+import contextlib
+import types
+
+import pytest
+import torch
+
+from xlstm_mlstm_cell_b200 import binding
+
+GIVEN = types.SimpleNamespace(cuda_stream=0x51, device=torch.device("cuda", 0), device_index=0, name="given")
+CALLER = types.SimpleNamespace(cuda_stream=0x52, device=torch.device("cuda", 0), device_index=0, name="caller")
+
+
+class Library:
+    """Every entry point succeeds; every size is 512 bytes."""
+
+    def __getattr__(self, name):
+        return lambda *a: 512 if name.endswith("_size") else 0
+
+
+@pytest.fixture
+def notes(monkeypatch):
+    """Allocations as (tensor, stream current at that moment) and the streams each was recorded on."""
+    made, recorded, current = [], {}, [CALLER]
+
+    @contextlib.contextmanager
+    def stream(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    def noting(make):
+        def wrapped(*a, **kw):
+            kw.pop("device", None)
+            t = make(*a, **kw)
+            made.append((t, current[-1]))
+            return t
+        return wrapped
+
+    for name in ("empty", "empty_like", "zeros"):
+        monkeypatch.setattr(torch, name, noting(getattr(torch, name)))
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.setdefault(id(t), []).append(s))
+    monkeypatch.setattr(binding, "load", lambda *a: Library())
+    monkeypatch.setattr(binding, "_cuda_index", lambda t: t.get_device())
+    monkeypatch.setattr(binding, "_on", lambda index, stream, call: call(0))
+    return made, recorded
+
+
+def rand(*shape):
+    return torch.randn(*shape)
+
+
+def delta(*lead):
+    q, v, g = rand(2, 1, *lead, 16), rand(2, 2, *lead, 24), rand(2, 2, *lead)
+    return q, q.clone(), v, g, g.clone()
+
+
+STATE = (2, 2, 16, 24)
+W = torch.ones(16)
+OPERATORS = {
+    "gdelta_fwd": (lambda **kw: binding.gdelta_fwd(*delta(5), **kw), 3),
+    "gdelta_fwd from a state": (lambda **kw: binding.gdelta_fwd(*delta(5), state=rand(*STATE), **kw), 3),
+    "gdelta_fwd without the state": (lambda **kw: binding.gdelta_fwd(*delta(5), return_state=False, **kw), 2),
+    "gdelta_step": (lambda **kw: binding.gdelta_step(rand(*STATE), *delta(), **kw), 1),
+    "gdelta_bwd": (lambda **kw: binding.gdelta_bwd(*delta(5), rand(2, 2, 5, 24), **kw), 6),
+    "gdelta_bwd from a state": (lambda **kw: binding.gdelta_bwd(*delta(5), rand(2, 2, 5, 24), state=rand(*STATE), **kw), 7),
+    "qknorm_fwd": (lambda **kw: binding.qknorm_fwd(rand(2, 5, 3, 16), rand(2, 5, 1, 16), **kw), 2),
+    "qknorm_bwd": (lambda **kw: binding.qknorm_bwd(rand(2, 3, 5, 16), rand(2, 1, 5, 16), rand(2, 5, 3, 16),
+                                                   rand(2, 5, 1, 16), q_weight=W, k_weight=W, **kw), 5),
+}
+
+
+def check_given_stream(call, tensors, notes):
+    made, recorded = notes
+    call(stream=GIVEN)
+    assert len(made) == tensors
+    for t, where in made:
+        assert where is GIVEN, "allocated on the current stream, used on the given one"
+        assert recorded.get(id(t)) == (None if t.dtype == torch.uint8 else [CALLER])   # workspaces are bytes
+
+
+@pytest.mark.parametrize("name", sorted(OPERATORS))
+def test_a_given_streams_call_allocates_from_that_stream(name, notes):
+    call, tensors = OPERATORS[name]
+    check_given_stream(call, tensors, notes)
+
+
+@pytest.mark.parametrize("name", sorted(OPERATORS))
+def test_a_call_on_the_current_stream_allocates_there(name, notes):
+    made, recorded = notes
+    call, tensors = OPERATORS[name]
+    call()
+    assert len(made) == tensors and all(where is CALLER for _, where in made) and not recorded

@@ -428,10 +428,24 @@ def gdelta_workspace_size(B, NH, NHV, S, DK, DV, dtype, backward: bool = False) 
 
 
 def _scratch(n, device, stream):
-    """A workspace for one call; on a stream of the caller's its memory outlives the call's work there."""
-    t = torch.empty(n, dtype=torch.uint8, device=device)
-    if stream is not None and n:
-        t.record_stream(stream)
+    """A workspace for one call.  With a stream of the caller's it comes from that stream's memory: a block of the
+    current stream's may still be in use by work queued there, for which the call's kernels do not wait."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _new(stream, make):
+    """``make()``, an output that a call allocates itself: from the memory of a given stream, as a workspace is, and
+    recorded on the current one, where the caller goes on to use it, so that its block is not handed on before that
+    is done either."""
+    if stream is None:
+        return make()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(caller)
     return t
 
 
@@ -462,13 +476,13 @@ def gdelta_fwd(q, k, v, g, beta, state=None, lengths=None, scale=None, o_out=Non
     if state is not None:
         _need("state", state, (B, NHV, DK, DV), torch.float32, index)
     if o_out is None:
-        o_out = torch.empty_like(v)
+        o_out = _new(stream, lambda: torch.empty_like(v))
     else:
         _need("o_out", o_out, v.shape, q.dtype, index)
     if state_out is not None:
         _need("state_out", state_out, (B, NHV, DK, DV), torch.float32, index)
     elif return_state:
-        state_out = torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device)
+        state_out = _new(stream, lambda: torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device))
     workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, False, stream)
     _check("gdelta_fwd", _on(index, stream, lambda s: lib.gdelta_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), dt, B, NH, NHV, S, DK,
@@ -484,7 +498,7 @@ def gdelta_step(state, q, k, v, g, beta, scale=None, o_out=None, stream=None):
     dt, B, NH, NHV, _, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, None, step=True)
     _need("state", state, (B, NHV, DK, DV), torch.float32, index)
     if o_out is None:
-        o_out = torch.empty_like(v)
+        o_out = _new(stream, lambda: torch.empty_like(v))
     else:
         _need("o_out", o_out, v.shape, q.dtype, index)
     _check("gdelta_step", _on(index, stream, lambda s: lib.gdelta_step(
@@ -505,8 +519,7 @@ def gdelta_bwd(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scal
         if t is not None:
             _need(name, t, (B, NHV, DK, DV), torch.float32, index)
     if out is None:
-        out = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
-               torch.empty_like(beta), None if state is None else torch.empty_like(state))
+        out = tuple(None if x is None else _new(stream, lambda: torch.empty_like(x)) for x in (q, k, v, g, beta, state))
     else:
         for name, t, x in zip(("dq", "dk", "dv", "dg", "dbeta"), out, (q, k, v, g, beta)):
             _need(name, t, x.shape, x.dtype, index)
@@ -576,11 +589,11 @@ def qknorm_fwd(q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: float
     lib = load()
     dt, B, S, NHQ, NHK, D, RD, kind, index = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
     if q_out is None:
-        q_out = torch.empty((B, NHQ, S, D), dtype=q.dtype, device=q.device)
+        q_out = _new(stream, lambda: torch.empty((B, NHQ, S, D), dtype=q.dtype, device=q.device))
     else:
         _need("q_out", q_out, (B, NHQ, S, D), q.dtype, index)
     if k_out is None:
-        k_out = torch.empty((B, NHK, S, D), dtype=q.dtype, device=q.device)
+        k_out = _new(stream, lambda: torch.empty((B, NHK, S, D), dtype=q.dtype, device=q.device))
     else:
         _need("k_out", k_out, (B, NHK, S, D), q.dtype, index)
     _check("qknorm_fwd", _on(index, stream, lambda s: lib.qknorm_fwd(
@@ -600,15 +613,15 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm: str = "
     _need("dq_out", dq_out, (B, NHQ, S, D), q.dtype, index)
     _need("dk_out", dk_out, (B, NHK, S, D), q.dtype, index)
     if out is None:
-        dq = torch.empty((B, S, NHQ, D), dtype=q.dtype, device=q.device)
-        dk = torch.empty((B, S, NHK, D), dtype=q.dtype, device=q.device)
+        dq = _new(stream, lambda: torch.empty((B, S, NHQ, D), dtype=q.dtype, device=q.device))
+        dk = _new(stream, lambda: torch.empty((B, S, NHK, D), dtype=q.dtype, device=q.device))
     else:
         dq, dk = out
         for name, t, x in (("dq", dq, q), ("dk", dk, k)):
             if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != index or (t.numel() and t.stride(3) != 1):
                 raise ValueError("%s must be like its input, the elements of a head contiguous" % name)
-    dwq = None if q_weight is None else torch.empty_like(q_weight)
-    dwk = None if k_weight is None else torch.empty_like(k_weight)
+    dwq = None if q_weight is None else _new(stream, lambda: torch.empty_like(q_weight))
+    dwk = None if k_weight is None else _new(stream, lambda: torch.empty_like(k_weight))
     if workspace is None:
         n = int(lib.qknorm_bwd_workspace_size(B, S, NHQ, NHK, D)) if (dwq is not None or dwk is not None) else 0
         workspace = _scratch(n, q.device, stream)

@@ -1,4 +1,4 @@
-"""Calls of the delta rule and the norms on a given stream beside calls on the current one, nothing synchronized in
+"""Calls of the delta rule, the norms and the cells on a given stream beside calls on the current one, nothing synchronized in
 between: what the binding allocates is shared by no two calls in flight.  The same inputs give the same bits, so
 every result is compared exactly with that of a call that ran alone."""
 from __future__ import annotations
@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from xlstm_mlstm_cell_b200 import binding
+from xlstm_mlstm_cell_b200.workloads import make_custom
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +27,18 @@ def norms(seed):
     return r(2, 4, 900, 128).cuda(), r(2, 2, 900, 128).cuda(), r(2, 900, 4, 128).cuda(), r(2, 900, 2, 128).cuda(), *w
 
 
+def cells(seed):
+    return [x.cuda() for x in make_custom(2, 4, 640, 128, 128, "bf16", seed=seed, ig=(-1.0, 2.0), fg=(4.0, 1.0))]
+
+
+def cell_fwd(x, **kw):
+    return binding.fwd(*x, **kw)
+
+
+def cell_bwd(x, **kw):
+    return binding.bwd(*x, x[2], **kw)
+
+
 def fwd(x, **kw):
     return binding.gdelta_fwd(*x[:5], **kw)
 
@@ -42,7 +55,7 @@ def norm_bwd(x, **kw):
     return binding.qknorm_bwd(*x, **kw)
 
 
-CALLS = [(fwd, delta), (bwd, delta), (norm_fwd, norms), (norm_bwd, norms)]
+CALLS = [(fwd, delta), (bwd, delta), (norm_fwd, norms), (norm_bwd, norms), (cell_fwd, cells), (cell_bwd, cells)]
 
 
 @pytest.mark.parametrize("call,make", CALLS)

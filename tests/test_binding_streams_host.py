@@ -52,6 +52,7 @@ def notes(monkeypatch):
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.setdefault(id(t), []).append(s))
     monkeypatch.setattr(binding, "load", lambda *a: Library())
     monkeypatch.setattr(binding, "_cuda_index", lambda t: t.get_device())
+    monkeypatch.setattr(binding, "_stream", lambda s: None)
     monkeypatch.setattr(binding, "_on", lambda index, stream, call: call(0))
     return made, recorded
 
@@ -80,6 +81,26 @@ OPERATORS = {
 }
 
 
+def cell(*lead):
+    q, v, g = rand(2, 1, *lead, 16), rand(2, 1, *lead, 16), rand(2, 1, *lead)
+    return q, q.clone(), v, g, g.clone()
+
+
+PARTS = rand(3, 2, 1, 16, 16), rand(3, 2, 1, 16), rand(3, 2, 1), rand(3, 2, 1)
+CELLS = {
+    "fwd": (lambda **kw: binding.fwd(*cell(5), **kw), 5),
+    "fwd with an output gate": (lambda **kw: binding.fwd(*cell(5), rand(2, 1, 5, 16), return_state=False, **kw), 2),
+    "bwd": (lambda **kw: binding.bwd(*cell(5), None, rand(2, 1, 5, 16), **kw), 6),
+    "bwd with an output gate": (lambda **kw: binding.bwd(*cell(5), rand(2, 1, 5, 16), rand(2, 1, 5, 16), **kw), 7),
+    "fwd_final_state": (lambda **kw: binding.fwd_final_state(*cell(5)[1:], **kw), 4),
+    "log_decay_sum": (lambda **kw: binding.log_decay_sum(rand(2, 1, 5), **kw), 1),
+    "state_prefix": (lambda **kw: binding.state_prefix(*PARTS, rank=1, **kw), 3),
+    "fwd_noalloc": (lambda **kw: binding.fwd_noalloc(*cell(5), **kw), 4),
+    "step": (lambda **kw: binding.step(rand(2, 1, 16, 16), rand(2, 1, 16), rand(2, 1), *cell(), **kw), 1),
+    "slstm_fwd": (lambda **kw: binding.slstm_fwd(rand(2, 5, 4, 1, 16), rand(1, 4, 16, 16), **kw), 5),
+}
+
+
 def check_given_stream(call, tensors, notes):
     made, recorded = notes
     call(stream=GIVEN)
@@ -95,9 +116,15 @@ def test_a_given_streams_call_allocates_from_that_stream(name, notes):
     check_given_stream(call, tensors, notes)
 
 
-@pytest.mark.parametrize("name", sorted(OPERATORS))
+@pytest.mark.parametrize("name", sorted(CELLS))
+def test_a_given_streams_cell_allocates_from_that_stream(name, notes):
+    call, tensors = CELLS[name]
+    check_given_stream(call, tensors, notes)
+
+
+@pytest.mark.parametrize("name", sorted(OPERATORS) + sorted(CELLS))
 def test_a_call_on_the_current_stream_allocates_there(name, notes):
     made, recorded = notes
-    call, tensors = OPERATORS[name]
+    call, tensors = {**OPERATORS, **CELLS}[name]
     call()
     assert len(made) == tensors and all(where is CALLER for _, where in made) and not recorded

@@ -121,6 +121,28 @@ def _check(fn, status):
         raise MlstmError(fn, status, _lib)
 
 
+def _scratch(n, device, stream):
+    """A workspace for one call.  With a stream of the caller's it comes from that stream's memory: a block of the
+    current stream's may still be in use by work queued there, for which the call's kernels do not wait."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _new(stream, make):
+    """``make()``, an output that a call allocates itself: from the memory of a given stream, as a workspace is, and
+    recorded on the current one, where the caller goes on to use it, so that its block is not handed on before that
+    is done either."""
+    if stream is None:
+        return make()
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(caller)
+    return t
+
+
 def workspace_size(B, NH, S, DHQK, DHV, chunk, dtype) -> int:
     dt = MLSTM_BF16 if dtype == torch.bfloat16 else MLSTM_F32
     return int(load().mlstm_fwd_workspace_size(B, NH, S, DHQK, DHV, chunk, dt))
@@ -150,11 +172,11 @@ def fwd_segments(B, NH, S, DHQK, DHV, chunk, dtype) -> int:
     return int(load().mlstm_fwd_segments(B, NH, S, DHQK, DHV, chunk, dt))
 
 
-def alloc_workspace(B, NH, S, DHQK, DHV, chunk, dtype, device="cuda") -> torch.Tensor:
+def alloc_workspace(B, NH, S, DHQK, DHV, chunk, dtype, device="cuda", stream=None) -> torch.Tensor:
     n = workspace_size(B, NH, S, DHQK, DHV, chunk, dtype)
     if n == 0:
         raise MlstmError("mlstm_fwd_workspace_size", 2)
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    return _scratch(n, device, stream)
 
 
 FWD_PHASES = 4
@@ -175,16 +197,16 @@ def fwd(q, k, v, igate, fgate, ogate=None, chunk: int = 64, h_out=None, C_final=
     DHV = v.shape[-1]
     dt = _dt(q)
     if h_out is None:
-        h_out = torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device)
+        h_out = _new(stream, lambda: torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device))
     if return_state:
         if C_final is None:
-            C_final = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device)
+            C_final = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device))
         if n_final is None:
-            n_final = torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device)
+            n_final = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device))
         if m_final is None:
-            m_final = torch.empty((B, NH), dtype=torch.float32, device=q.device)
+            m_final = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=q.device))
     if workspace is None:
-        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, q.dtype, q.device)
+        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, q.dtype, q.device, stream)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _ptr(ogate), dt, B, NH, S, DHQK, DHV, chunk,
             _ptr(h_out), _ptr(C_final), _ptr(n_final), _ptr(m_final), _ptr(workspace), workspace.numel(),
             _stream(stream))
@@ -225,14 +247,14 @@ def bwd(q, k, v, igate, fgate, ogate, dh, chunk: int = 64, workspace=None, strea
     DHV = v.shape[-1]
     dt = _dt(q)
     if out is None:
-        out = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(igate),
-               torch.empty_like(fgate), None if ogate is None else torch.empty_like(ogate))
+        out = tuple(None if x is None else _new(stream, lambda: torch.empty_like(x))
+                    for x in (q, k, v, igate, fgate, ogate))
     dq, dk, dv, dig, dfg, dog = out
     if workspace is None:
         n = bwd_workspace_size(B, NH, S, DHQK, DHV, chunk, q.dtype)
         if n == 0:
             raise MlstmError("mlstm_bwd_workspace_size", 2)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(n, q.device, stream)
     _check("mlstm_bwd", lib.mlstm_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _ptr(ogate), _ptr(dh), dt,
                                       B, NH, S, DHQK, DHV, chunk, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dig), _ptr(dfg),
                                       _ptr(dog), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -244,11 +266,11 @@ def fwd_final_state(k, v, igate, fgate, chunk: int = 64, workspace=None, stream=
     lib = load()
     B, NH, S, DHQK = k.shape
     DHV = v.shape[-1]
-    C = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=k.device)
-    n = torch.empty((B, NH, DHQK), dtype=torch.float32, device=k.device)
-    m = torch.empty((B, NH), dtype=torch.float32, device=k.device)
+    C = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=k.device))
+    n = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=k.device))
+    m = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=k.device))
     if workspace is None:
-        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, k.dtype, k.device)
+        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, k.dtype, k.device, stream)
     _check("mlstm_fwd_final_state",
            lib.mlstm_fwd_final_state(_ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _dt(k), B, NH, S, DHQK, DHV, chunk,
                                      _ptr(C), _ptr(n), _ptr(m), _ptr(workspace), workspace.numel(), _stream(stream)))
@@ -259,7 +281,7 @@ def log_decay_sum(fgate, stream=None):
     """mlstm_log_decay_sum: per (b, h) the sum over tokens of logsigmoid(f~), ``[B, NH]``."""
     lib = load()
     B, NH, S = fgate.shape
-    g = torch.empty((B, NH), dtype=torch.float32, device=fgate.device)
+    g = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=fgate.device))
     _check("mlstm_log_decay_sum", lib.mlstm_log_decay_sum(_ptr(fgate), B, NH, S, _ptr(g), _stream(stream)))
     return g
 
@@ -270,9 +292,9 @@ def state_prefix(C_parts, n_parts, m_parts, g_parts, rank: int, stream=None):
     ``g_parts [R, B, NH]``."""
     lib = load()
     R, B, NH, DHQK, DHV = C_parts.shape
-    C0 = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=C_parts.device)
-    n0 = torch.empty((B, NH, DHQK), dtype=torch.float32, device=C_parts.device)
-    m0 = torch.empty((B, NH), dtype=torch.float32, device=C_parts.device)
+    C0 = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=C_parts.device))
+    n0 = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=C_parts.device))
+    m0 = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=C_parts.device))
     _check("mlstm_state_prefix",
            lib.mlstm_state_prefix(_ptr(C_parts), _ptr(n_parts), _ptr(m_parts), _ptr(g_parts), R, rank, B, NH, DHQK,
                                   DHV, _ptr(C0), _ptr(n0), _ptr(m0), _stream(stream)))
@@ -293,13 +315,13 @@ def fwd_noalloc(q, k, v, igate, fgate, ogate=None, chunk: int = 64, h_out=None, 
     B, NH, S, DHQK = q.shape
     DHV = v.shape[-1]
     if h_out is None:
-        h_out = torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device)
+        h_out = _new(stream, lambda: torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device))
     if C_final is None:
-        C_final = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device)
+        C_final = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device))
     if n_final is None:
-        n_final = torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device)
+        n_final = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device))
     if m_final is None:
-        m_final = torch.empty((B, NH), dtype=torch.float32, device=q.device)
+        m_final = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=q.device))
     st = lib.mlstm_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _ptr(ogate), _dt(q), B, NH,
                                S, DHQK, DHV, chunk, _ptr(h_out), _ptr(C_final), _ptr(n_final), _ptr(m_final),
                                _stream(stream))
@@ -323,7 +345,7 @@ def step(C, n, m, q, k, v, igate, fgate, ogate=None, h_out=None, stream=None):
     B, NH, DHQK = q.shape
     DHV = v.shape[-1]
     if h_out is None:
-        h_out = torch.empty((B, NH, DHV), dtype=q.dtype, device=q.device)
+        h_out = _new(stream, lambda: torch.empty((B, NH, DHV), dtype=q.dtype, device=q.device))
     st = lib.mlstm_step(_ptr(C), _ptr(n), _ptr(m), _ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate),
                         _ptr(ogate), _dt(q), B, NH, DHQK, DHV, _ptr(h_out), _stream(stream))
     _check("mlstm_step", st)
@@ -343,10 +365,11 @@ def slstm_fwd(wx, R, forget: str = "exp", state=None, h_out=None, want_h: bool =
     lib = load()
     B, S, _, NH, DH = wx.shape
     if state is None:
-        state = tuple(torch.zeros((B, NH, DH), dtype=torch.float32, device=wx.device) for _ in range(4))
+        zeros = lambda: torch.zeros((B, NH, DH), dtype=torch.float32, device=wx.device)   # noqa: E731 - on the call's stream
+        state = tuple(_new(stream, zeros) for _ in range(4))
     c, n, m, h = state
     if want_h and h_out is None:
-        h_out = torch.empty((B, S, NH, DH), dtype=wx.dtype, device=wx.device)
+        h_out = _new(stream, lambda: torch.empty((B, S, NH, DH), dtype=wx.dtype, device=wx.device))
     st = lib.slstm_fwd(_ptr(wx), _ptr(R), _dt(wx), B, S, NH, DH, 1 if forget == "sigmoid" else 0, _ptr(c), _ptr(n),
                        _ptr(m), _ptr(h), _ptr(h_out if want_h else None), _ptr(status), _stream(stream))
     _check("slstm_fwd", st)
@@ -425,28 +448,6 @@ def gdelta_workspace_size(B, NH, NHV, S, DK, DV, dtype, backward: bool = False) 
     lib, dt = load(), MLSTM_BF16 if dtype == torch.bfloat16 else MLSTM_F32
     size = lib.gdelta_bwd_workspace_size if backward else lib.gdelta_fwd_workspace_size
     return int(size(B, NH, NHV, S, DK, DV, dt))
-
-
-def _scratch(n, device, stream):
-    """A workspace for one call.  With a stream of the caller's it comes from that stream's memory: a block of the
-    current stream's may still be in use by work queued there, for which the call's kernels do not wait."""
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
-
-
-def _new(stream, make):
-    """``make()``, an output that a call allocates itself: from the memory of a given stream, as a workspace is, and
-    recorded on the current one, where the caller goes on to use it, so that its block is not handed on before that
-    is done either."""
-    if stream is None:
-        return make()
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        t = make()
-    t.record_stream(caller)
-    return t
 
 
 def _gdelta_workspace(workspace, sizes, device, index, backward, stream):

@@ -10,6 +10,9 @@
  *       p + RD / 2 (or 2 p and 2 p + 1 with `interleaved`), turns by the angle
  *       position * inv_freq[p]:  (a, b) -> (a cos - b sin, a sin + b cos).
  *
+ * The squares are summed in fp32, which holds those of elements between about 1e-19 and 1e19 / sqrt(D): what eps does
+ * not carry has to lie there.  eps may be 0, but a vector of zeros then has no norm (its r is infinite).
+ *
  * The angle is formed and reduced in fp64 (a position of 131072 times a frequency of one
  * has no fraction left in fp32); everything else is fp32, rounded once to `dt`.
  *

@@ -1,6 +1,6 @@
 // qknorm.cu -- norms of queries and keys per head with the position rotation, forward and backward:
 //   r = 1 / sqrt(mean|sum(x^2) + eps),  z = r w x,  y = z with pairs of its first RD elements rotated;
-//   d = inverse rotation of dy,  dw = sum of d r x,  dx = r (w d - r^2 x mean|sum(w d x)).
+//   d = inverse rotation of dy,  xh = r x,  dw = sum of d xh,  dx = r (w d - xh mean|sum(w d xh)).
 //
 // Bound by HBM: every vector is read once and written once (the backward reads two).  A group of lanes
 // takes a token and goes through its heads; each lane holds units of VEC + VEC elements of a vector, chosen
@@ -302,7 +302,9 @@ MLSTM_DEVINL void one_side(const Params &p, const Side &sd, const Place<VEC, SPA
                 }
         }
         const float r = rsqrtf(fmaf(s, inv_n, p.eps));
-        const float back = BWD ? -r * r * r * (xd * inv_n) : 0.f;
+        // dx = r (w d - (r x) mean|sum(w d (r x))): with r x, whose size is about one, and never r^3, which leaves
+        // fp32 where r itself is far inside it
+        const float back = BWD ? -r * (r * xd * inv_n) : 0.f;
         const uint64_t r2 = f2_pack(r, r), back2 = f2_pack(back, back);
 #pragma unroll
         for (int n = 0; n < NU; ++n) {
@@ -310,8 +312,9 @@ MLSTM_DEVINL void one_side(const Params &p, const Side &sd, const Place<VEC, SPA
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 if (BWD) {
-                    gw[n * VEC + e] = f2_fma(gwd[n][e], f2_mul(r2, xv[n][e]), gw[n * VEC + e]);
-                    xv[n][e] = f2_fma(r2, d[n][e], f2_mul(back2, xv[n][e]));
+                    const uint64_t xh = f2_mul(r2, xv[n][e]);
+                    gw[n * VEC + e] = f2_fma(gwd[n][e], xh, gw[n * VEC + e]);
+                    xv[n][e] = f2_fma(r2, d[n][e], f2_mul(back2, xh));
                 } else {
                     xv[n][e] = f2_mul(xv[n][e], f2_mul(r2, w[n][e]));
                 }

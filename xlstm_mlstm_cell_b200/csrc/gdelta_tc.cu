@@ -211,6 +211,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (c == 0 && bh == 0 && blockIdx.z == 0 && tid == 0) *w.status = 0u;
     const int len = min(CH, live_tokens(lengths, b, S) - c * CH);
     if (len > 0) {
+        bool issued = false;
         if (tid == 0) {
             mbar_arrive_expect_tx(&bars[0], 32768);
             for (int kb = 0; kb < 2; ++kb) {
@@ -225,6 +226,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     mma_ss(tmem, dk, dk, ID, kk > 0);
                 }
                 mma_commit(&bars[1]);
+                issued = true;
             }
         }
         __syncwarp();
@@ -369,7 +371,10 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             __syncthreads();
         }
-        if (!ok && tid == 0) mbar_wait_drain(&bars[0], 0);
+        if (tid == 0 && !ok) {   // a wait gave up: let the copies and the MMAs of this CTA finish (bounded)
+            mbar_wait_drain(&bars[0], 0);
+            if (issued) mbar_wait_drain(&bars[1], 0);
+        }
     }
     tc_fence_before();
     __syncthreads();

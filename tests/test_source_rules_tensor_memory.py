@@ -30,3 +30,20 @@ def test_tensor_memory_is_freed_after_the_mmas():
         assert waits or commits & drains, "%s: MMAs commit to %s, drained are %s" % (name, sorted(commits), sorted(drains))
         found += 1
     assert found >= 8
+
+
+def test_mmas_are_ordered_behind_the_waits_before_them():
+    """In the delta rule's kernels an MMA that follows a wait for other threads has the fence between the two that
+    orders tensor-memory operations behind the wait: those threads may have read the accumulator it writes.
+    (The preparation's MMAs wait for a copy alone.)"""
+    found = 0
+    for name, body in kernels():
+        if not name.startswith("gdelta"):
+            continue
+        for m in re.finditer(r"\bmma_ss\(", body):
+            wait = body.rindex("mbar_wait(", 0, m.start())
+            if body[wait:].startswith("mbar_wait(&bars[0]"):
+                continue
+            assert "tc_fence_after" in body[wait:m.start()], "%s: no fence behind %s" % (name, body[wait:].split(";")[0])
+            found += 1
+    assert found >= 8

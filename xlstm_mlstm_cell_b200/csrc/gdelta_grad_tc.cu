@@ -212,6 +212,7 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 mma_ss(tmem + CZ, da + (uint64_t)(PA[q] * 1024 + k * 2), ds + (uint64_t)(PB[q] * 1024 + k * 2), IDN,
                                        s % SUM + q + k > 0);
                         mbar_wait(e_ready, n & 1u, wc);
+                        tc_fence_after();
 #pragma unroll
                         for (int q = 0; q < 6; ++q)
 #pragma unroll
@@ -220,6 +221,7 @@ grad_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                        s + q % 5 + k > 0);
                         mma_commit(z_done);   // and HX: [dO; dV] and S are free
                         mbar_wait(d_ready, n & 1u, wc);
+                        tc_fence_after();   // W goes over sums that the workers have just read
                         // E in rows 64..127; the rows in front of a part read what lies before it, into lanes nothing uses
 #pragma unroll
                         for (int q = 0; q < 6; ++q)

@@ -52,7 +52,7 @@ extern "C" {
  * Bytes of device workspace gdelta_fwd needs (0 when the arguments are unsupported):
  * a status word, 8 bytes of gates per token of a whole chunk and value head, and per
  * chunk and value head the two 64 x 64 matrices T and the scores in fp32 (32 KB), or
- * on the tensor-core path T and the scores' product with it as bf16 parts (32 KB).
+ * on the tensor-core path T and the scores' product with it as bf16 parts (40 KB).
  */
 size_t gdelta_fwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, mlstm_dtype dt);
 
@@ -62,10 +62,10 @@ size_t gdelta_fwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, 
  * the state).  workspace: gdelta_fwd_workspace_size() bytes, 256-byte aligned, not
  * shared by two calls in flight.
  *
- * Accuracy: sums and the state are fp32.  On the tensor-core path (bf16 inputs,
- * gdelta_fwd_tensor_path) every fp32 operand of a product enters as bf16 parts, value
- * and rounding residue, so that a state from bf16 inputs is as close to an fp64
- * evaluation as fp32 arithmetic brings it (about 1e-6); mlstm_fwd_status on the
+ * Accuracy: sums and the state are fp32.  On the tensor-core path (bf16 inputs, gdelta_fwd_tensor_path) every
+ * fp32 operand that the state comes of enters its products as three bf16 parts, which hold its 24 bits, so that a
+ * state from bf16 inputs is as close to an fp64 evaluation as fp32 arithmetic brings it (within 5e-7 where nothing
+ * cancels); the scores' product, which only the bf16 o sees, as two.  mlstm_fwd_status on the
  * workspace tells whether every bounded wait of its kernels completed.
  */
 mlstm_status gdelta_fwd(const void *q, const void *k, const void *v, const float *g, const float *beta,

@@ -49,6 +49,7 @@ size_t plan(char *base, const Args &a, bool backward, Workspace *w)
     if (tc) {
         w->GB = reinterpret_cast<float2 *>(take(sizeof(float2) * 64 * chunks));
         w->TG = reinterpret_cast<uint8_t *>(take(32768 * chunks));
+        w->TL = reinterpret_cast<uint8_t *>(take(8192 * chunks));
     } else {
         w->T = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
     }
@@ -57,7 +58,6 @@ size_t plan(char *base, const Args &a, bool backward, Workspace *w)
         w->P = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
     }
     if (backward) {
-        if (tc) w->TL = reinterpret_cast<uint8_t *>(take(8192 * chunks));
         if (tc && a.DK <= 64) w->GL = reinterpret_cast<uint8_t *>(take(8192 * chunks));
         w->KK = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
         w->SC = reinterpret_cast<float *>(take(sizeof(float) * a.DK * a.DV * chunks));

@@ -15,11 +15,13 @@
 // Operands.  K and Q are stacked in shared memory, 64 rows each, so that one M = 128 MMA serves both;
 // the same tile, read MN-major, is the A operand of the state's update.  The fp32 operands S, Y and the
 // state update's enter as three bf16 parts each, which hold all 24 bits, side by side along N: one MMA
-// reads A once for all three, and the epilogue adds the parts' columns.  T - I and G enter as two parts,
-// value and rounding residue (rms error 2.7e-6 of the correction they carry), T - I in the backward's forward
-// walk as three: dg and dbeta are fp32 outputs, and two parts alone put 4e-7 (DK 128) to 7e-7 (DK 64) into dg
-// through E, against 1e-7 through dV; G likewise where DK is at most 64.  K, Q, dO are exact.  Without its unit diagonal T leaves Y itself out of the
-// MMA: the threads that formed Y in fp32 add it to the result.  The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
+// reads A once for all three, and the epilogue adds the parts' columns.  T - I enters as three parts where the state
+// or E come of it: two (value and rounding residue, 2.5e-6 of the correction) leave the state of slowly forgetting gates
+// 5.5e-7 off where fp32 arithmetic is 1.6e-7, and that of a key that repeats, whose sums nearly cancel, 3e-5 off where
+// it is 5e-7.  Forward the third part costs 0.26 us a chunk of 2.1 (its four MMAs a chain).  G enters as two, which
+// only the bf16 o sees; reverse T - I as two as well, and G as three where DK is at most 64.  K, Q, dO are exact.
+// Without its unit diagonal T leaves Y itself out of the MMA: the threads that formed Y in fp32 add it to the result.
+// The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
 // each, and takes the update with fp32 additions.
 //
 // Roles: warp 0 one TMA thread, warp 1 the MMA thread (and the TMEM allocation), then 4 epilogue warps per
@@ -41,6 +43,12 @@ MLSTM_DEVINL void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                  ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+
+// Asks for the same bytes to be brought to L2.
+MLSTM_DEVINL void bulk_prefetch(const void *src, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // Eight pairs of values of a row as three bf16 parts, whose sum is exactly the fp32 value: the top 8
@@ -91,7 +99,7 @@ MLSTM_DEVINL void load_parts(uint32_t taddr, uint32_t step, uint64_t (&x)[8])
 
 namespace prep {
 constexpr int THREADS = 128;
-constexpr uint32_t KQ = 0;                              // [2 blocks][128 rows][64] K over Q, until its product is done; then
+// from 0: [2 blocks][128 rows][64] K over Q, until its product is done; then
 constexpr uint32_t MR = 0;                              // [64][LDT] floats: I + KK diag(beta), then T, row-major
 constexpr uint32_t MC = MR + 64 * LDT * 4;              // [64][LDT] its transpose
 constexpr uint32_t PC = MC + 64 * LDT * 4;              // [64][LDT] transpose of P diag(beta)
@@ -356,7 +364,7 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
                     *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
                     *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
-                    if (BACKWARD && (part == 0 || w.GL)) {   // the backward's third part of T - I, and of G where there is room
+                    if (part == 0 || (BACKWARD && w.GL)) {   // the third part of T - I, and the backward's of G where there is room
                         float z[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -387,8 +395,8 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 // ---------------------------------------------------------------- walk
 
 // A CTA runs two chains side by side, CW value columns each, on the same K, Q, T and G tiles: while the
-// epilogue warps of one pass over an accumulator, the MMAs of the other run.  What bounds a walk is that chain: 2.1 us
-// a chunk at CW 16 (32 heads of 16384 tokens, 128 x 128: 548 us, 128 CTAs); with the states
+// epilogue warps of one pass over an accumulator, the MMAs of the other run.  What bounds a walk is that chain: 2.4 us
+// a chunk at CW 16 (32 heads of 16384 tokens, 128 x 128: 605 us, 128 CTAs); with the states
 // and E kept 2.6 us, at CW 32 4.6 us (4 x 16 heads of 4096 tokens: 292 us, against 338 in two rounds of CTAs at CW
 // 16); reverse 3.2 us.  The tensor pipe is busy a quarter of it, the rest are the epilogues' passes from TMEM over registers to shared memory and the
 // waits between the two.  One chain of 32 columns, three or four chains, or 8 columns a thread were no faster.
@@ -401,22 +409,28 @@ struct Walk {
     static constexpr int EPI = 4 * (CW / 16);              // epilogue warps per chain, 16 columns each
     static constexpr int THREADS = 64 + 32 * NCH * EPI;
     static constexpr int STAGES = 2;
-    // A stage: [K; Q] as one or two blocks of 64 columns, then [T - I; G] values and residues, 16 KB each.  KEEP has
+    // A stage: [K; Q] as one or two blocks of 64 columns, then [T - I; G] values and residues, 16 KB each; forward
+    // also the third part of T - I, with zeros in G's rows.  With 64 columns a CTA there is room for T - I and G
+    // only once: the next chunk's come behind this one's second product with them (single).  KEEP has
     // no use for Q and G, whose lanes' sums stay unread: K alone, and three parts of T - I, 8 KB each; the MMAs' rows
     // 64..127 are then whatever follows, and so are the state's rows from 64 on with one block.  Reverse, a stage of
     // one block has room for G's third part.
-    static constexpr uint32_t KROWS = MODE == KEEP ? 64 : 128, KB = KROWS * 128, KBLK = KS / 4, TOFF = KBLK * KB;
-    static constexpr bool G3 = MODE == REVERSE && KS == 4;
-    static constexpr uint32_t STAGE = TOFF + (MODE == KEEP ? 24576 : 32768) + (G3 ? 8192 : 0);
+    static constexpr uint32_t KROWS = MODE == KEEP ? 64 : 128, KB = KROWS * 128, KBLK = KS / 4;
+    static constexpr bool G3 = MODE == REVERSE && KS == 4, SINGLE = MODE == FORWARD && CW == 32;
+    static constexpr uint32_t KQ = KBLK * KB;
+    static constexpr uint32_t TLOAD = (MODE == KEEP ? 24576 : 32768) + (MODE == FORWARD || G3 ? 8192 : 0);
+    static constexpr uint32_t TSIZE = TLOAD + (MODE == FORWARD ? 8192 : 0);
+    static constexpr uint32_t STAGE = KQ + (SINGLE ? 0 : TSIZE);
+    static constexpr uint32_t TOFF = SINGLE ? STAGES * STAGE : KQ;   // of a stage's, or of the only one
     static constexpr uint32_t BLOCKS = (3 * CW + 63) / 64; // blocks of 64 columns that hold an operand's parts
-    static constexpr uint32_t SP = STAGES * STAGE;         // per chain: S parts, 128 rows
+    static constexpr uint32_t SP = STAGES * STAGE + (SINGLE ? TSIZE : 0);   // per chain: S parts, 128 rows
     static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
     static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : 64;   // (reverse: K's tokens, then Q's)
     static constexpr uint32_t DO = YN + NCH * BLOCKS * YROWS * 128; // reverse: dO, 64 rows, the chains side by side
     // the backward: an epilogue warp's 32 rows of fp32 results on their way out
     static constexpr uint32_t OUT = DO + (MODE == REVERSE ? 8192 : 0);
     static constexpr uint32_t BAR = OUT + (MODE == FORWARD ? 0 : NCH * EPI * 2048);
-    static constexpr uint32_t NBAR = 2 * STAGES + 7 * NCH;
+    static constexpr uint32_t NBAR = 2 * STAGES + 7 * NCH + 2;
     static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
     static_assert(TOTAL <= 232448, "one CTA's shared memory");
     // TMEM columns of a chain: X and [E; F], 3 CW each; D over X, or (reverse) beside them with G^T dO
@@ -449,7 +463,8 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + W::BAR);
     // per chain: S, Y and N written by the epilogue; X, [E; F] and D finished by the MMAs
     uint64_t *full = bars, *empty = bars + NST, *s_ready = bars + 2 * NST, *x_done = s_ready + NCH, *y_ready = x_done + NCH,
-             *e_done = y_ready + NCH, *n_ready = e_done + NCH, *d_done = n_ready + NCH, *o_ready = d_done + NCH;
+             *e_done = y_ready + NCH, *n_ready = e_done + NCH, *d_done = n_ready + NCH, *o_ready = d_done + NCH,
+             *t_full = o_ready + NCH, *t_empty = t_full + 1;   // T - I and G where they have one place
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + W::NBAR), *abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bhv = blockIdx.y, b = bhv / p.NHV, bh = b * p.NH + (bhv % p.NHV) / (p.NHV / p.NH);
@@ -468,6 +483,8 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_init(&d_done[h], 1);
             mbar_init(&o_ready[h], W::EPI / 2);
         }
+        mbar_init(t_full, 1);
+        mbar_init(t_empty, 1);
         *abort_flag = 0u;
         fence_barrier_init();
         tma_prefetch(&tm_q);
@@ -476,6 +493,11 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             tma_prefetch(&tm_s);
             tma_prefetch(&tm_t);
         }
+    }
+    if (MODE == FORWARD) {   // the zeros behind the third part of T - I
+        for (uint32_t i = threadIdx.x * 16; i < (W::SINGLE ? 1 : NST) * 8192; i += W::THREADS * 16)
+            *reinterpret_cast<uint4 *>(smem + W::TOFF + (i >> 13) * W::STAGE + W::TLOAD + (i & 8191)) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async();
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, W::TMEM_COLS);
@@ -497,19 +519,29 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const int st = c % NST, ci = MODE == REVERSE ? nc - 1 - c : c;
                 if (c >= NST && !mbar_wait(&empty[st], (uint32_t)(c / NST - 1) & 1u, wc)) break;
                 uint8_t *s = smem + st * W::STAGE;
-                mbar_arrive_expect_tx(&full[st], W::STAGE);
+                const size_t ch = (size_t)bhv * p.w.NC + ci;
+                mbar_arrive_expect_tx(&full[st], W::KQ + (W::SINGLE ? 0 : W::TLOAD));
                 for (int kb = 0; kb < (int)W::KBLK; ++kb) {
                     tma_load_3d(s + kb * W::KB, &tm_k, 64 * kb, ci * CH, bh, &full[st]);
                     if (MODE != KEEP) tma_load_3d(s + kb * W::KB + 8192, &tm_q, 64 * kb, ci * CH, bh, &full[st]);
                 }
-                const size_t ch = (size_t)bhv * p.w.NC + ci;
+                uint64_t *tbar = &full[st];
+                uint8_t *tt = s + W::TOFF;
+                if (W::SINGLE) {
+                    bulk_prefetch(p.w.TG + ch * 32768, 32768);
+                    bulk_prefetch(p.w.TL + ch * 8192, 8192);
+                    if (c > 0 && !mbar_wait(t_empty, (uint32_t)(c - 1) & 1u, wc)) break;
+                    tbar = t_full;
+                    tt = smem + W::TOFF;
+                    mbar_arrive_expect_tx(t_full, W::TLOAD);
+                }
                 if (MODE == KEEP) {
-                    bulk_load(s + W::TOFF, p.w.TG + ch * 32768, 8192, &full[st]);
-                    bulk_load(s + W::TOFF + 8192, p.w.TG + ch * 32768 + 16384, 8192, &full[st]);
-                    bulk_load(s + W::TOFF + 16384, p.w.TL + ch * 8192, 8192, &full[st]);
+                    bulk_load(tt, p.w.TG + ch * 32768, 8192, tbar);
+                    bulk_load(tt + 8192, p.w.TG + ch * 32768 + 16384, 8192, tbar);
+                    bulk_load(tt + 16384, p.w.TL + ch * 8192, 8192, tbar);
                 } else {
-                    bulk_load(s + W::TOFF, p.w.TG + ch * 32768, 32768, &full[st]);
-                    if (W::G3) bulk_load(s + W::TOFF + 32768, p.w.GL + ch * 8192, 8192, &full[st]);
+                    bulk_load(tt, p.w.TG + ch * 32768, 32768, tbar);
+                    if (MODE == FORWARD || W::G3) bulk_load(tt + 32768, (W::G3 ? p.w.GL : p.w.TL) + ch * 8192, 8192, tbar);
                 }
             }
         }
@@ -532,7 +564,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             bool ok = true;
             for (int c = 0; c < nc && ok; ++c) {
                 const int st = c % NST;
-                const uint64_t so = (uint64_t)st * (W::STAGE / 16);
+                const uint64_t so = (uint64_t)st * (W::STAGE / 16), to = W::SINGLE ? 0 : so;
                 const uint32_t ph = (uint32_t)c & 1u;
                 ok = mbar_wait(&full[st], (uint32_t)(c / NST) & 1u, wc);
                 auto issue_x = [&](int h) {
@@ -551,35 +583,40 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (W::G3) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_ss(tmem + h * W::TCH + W::TG, atm + so + (uint64_t)(2048 + k * 128),
+                            mma_ss(tmem + h * W::TCH + W::TG, atm + to + (uint64_t)(2048 + k * 128),
                                    bo + (uint64_t)(h * CW / 8 + k * 128), IDG, k > 0);
                     }
 #pragma unroll
                     for (int k = 7; k >= 0; --k)   // G's rows lie 8 KB into the values' tile, and 16 KB further its residues'
-                        mma_ss(tmem + h * W::TCH + W::TG, atm + so + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
+                        mma_ss(tmem + h * W::TCH + W::TG, atm + to + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
                                bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, W::G3 || k < 7);
 #pragma unroll
                     for (int k = 4; k < 8; ++k)
                         mma_ss(tmem + h * W::TCH + W::TD, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 4);
                 };
                 auto issue_e = [&](int h) {
+                    if (W::SINGLE && h == 0 && !(ok = ok && mbar_wait(t_full, ph, wc))) return;
                     if (!(ok = ok && mbar_wait(&y_ready[h], ph, wc))) return;
                     tc_fence_after();
                     const uint32_t de = tmem + h * W::TCH + W::TE;
+                    // the smallest products first: an MMA cuts off at the size of the sum it adds to.  The residues of
+                    // T - I and G, without Y's third part (but for the first, which writes all columns)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ss(de, MODE == REVERSE ? atm + so + (uint64_t)(k * 128) : at + so + (uint64_t)(k * 2),
-                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDD : IDX, k > 0);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)   // the residues of T - I and G, without Y's third part
-                        mma_ss(de, MODE == REVERSE ? atm + so + (uint64_t)(1024 + k * 128) : at + so + (uint64_t)(RES + k * 2),
-                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDTM : IDM, 1);
-                    if (MODE == KEEP) {
+                        mma_ss(de, MODE == REVERSE ? atm + to + (uint64_t)(1024 + k * 128) : at + to + (uint64_t)(RES + k * 2),
+                               by + (uint64_t)(h * BY + k * 128),
+                               MODE == REVERSE ? (k ? IDTM : IDD) : (k ? IDM : IDX), k > 0);
+                    if (MODE != REVERSE) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)   // the third part of T - I with Y's first
-                            mma_ss(de, at + so + (uint64_t)(2 * RES + k * 2), by + (uint64_t)(h * BY + k * 128), IDG0, 1);
+                            mma_ss(de, at + to + (uint64_t)(2 * RES + k * 2), by + (uint64_t)(h * BY + k * 128), IDG0, 1);
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(de, MODE == REVERSE ? atm + to + (uint64_t)(k * 128) : at + to + (uint64_t)(k * 2),
+                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDD : IDX, 1);
                     mma_commit(&e_done[h]);
+                    if (W::SINGLE && h == NCH - 1) mma_commit(t_empty);
                 };
                 auto issue_d = [&](int h) {
                     if (!(ok = ok && mbar_wait(&n_ready[h], ph, wc))) return;

@@ -106,8 +106,9 @@ mlstm_status gdelta_step(float *state, const void *q, const void *k, const void 
  * workspace: gdelta_bwd_workspace_size() bytes, 256-byte aligned, not shared by two
  * calls in flight (the states at the chunks' starts and their gradients, 8 DK DV bytes
  * per chunk and value head, and 8 DV bytes per token and value head make up most of
- * it).  Accuracy on the tensor-core path: dg and dbeta about 1e-6 off an fp64
- * evaluation of the same inputs.
+ * it).  Accuracy on the tensor-core path: dS0 within 6e-7, dg and dbeta within 1.25e-6 of
+ * an fp64 evaluation of the same inputs, where they are not what is left of sums that nearly
+ * cancel (one key, repeated: as far as inputs moved by a step of fp32 would put fp64 itself).
  */
 size_t gdelta_bwd_workspace_size(int B, int NH, int NHV, int S, int DK, int DV, mlstm_dtype dt);
 mlstm_status gdelta_bwd(const void *q, const void *k, const void *v, const float *g, const float *beta,

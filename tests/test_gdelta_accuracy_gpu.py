@@ -7,6 +7,9 @@ MMAs of a product, half its final size on average.  A chunk's contribution to th
 eight MMAs (4.5 times its size in all), (T - I) Y in four of full size (2.5; those of the second and third parts of
 T - I come first and are small), K^T N in four (2.5): 9.5 * 0.69 h = 6.6 h if every one of them acts on all of the result.
 The eight roundings of the passes in between are independent, 0.41 h each: 1.2 h.  STATE = 8 h = 4.8e-7, for the state.
+Backwards the last product takes Q's tokens too, eight MMAs: 7.9 h and 1.2 h, DSTATE = 10 h = 6.0e-7, for the initial
+state's gradient.  The gradients of the gates and of beta multiply what the two walks left, 18 h, in products of eight MMAs of
+full size between two additions in registers, 3 h: GATES = 21 h = 1.25e-6.
 """
 from __future__ import annotations
 
@@ -20,7 +23,7 @@ from xlstm_mlstm_cell_b200 import binding
 pytestmark = pytest.mark.gpu
 
 H = 2.0 ** -24
-STATE = 8 * H
+STATE, DSTATE, GATES = 8 * H, 10 * H, 21 * H
 BF16 = 2.0 ** -8 / 3 ** 0.5   # the error of one rounding is spread evenly over half a step to either side
 
 
@@ -76,3 +79,32 @@ def test_state_of_a_repeated_key(DK, B):
     mS = oracle.gdelta_fwd(*(moved(t, gen) for t in x), state=moved(S0, gen))[1]
     torch.cuda.synchronize()
     assert_close("state", S, rS, STATE + 4 * float((mS - rS).norm() / rS.norm()))
+
+
+NAMES = ("dq", "dk", "dv", "dg", "dbeta", "dstate0")
+BOUNDS = (BF16, BF16, BF16, GATES, GATES, DSTATE)
+
+
+@pytest.mark.parametrize("rate", [0.0, 0.02, 0.2, 1.0])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_gradients(shape, rate):
+    x, do, S0, dS = make(*shape, rate, seed=shape[3] + 1)
+    got = binding.gdelta_bwd(*x, do, state=S0, dstate=dS)
+    ref = oracle.gdelta_bwd(*x, do, state=S0, dstate=dS)
+    torch.cuda.synchronize()
+    for name, a, b, bound in zip(NAMES, got, ref, BOUNDS):
+        assert_close(name, a, b, bound)
+
+
+@pytest.mark.parametrize("B", [1, 40])
+@pytest.mark.parametrize("DK", [64, 128])
+def test_gradients_of_a_repeated_key(DK, B):
+    """As for the state; seven products stand behind a gradient of a gate: those of the two walks, and its own."""
+    x, do, S0, dS = make(B, 2, 4, 300, DK, 128, 0.0, seed=DK + 1, same=True)
+    got = binding.gdelta_bwd(*x, do, state=S0, dstate=dS)
+    ref = oracle.gdelta_bwd(*x, do, state=S0, dstate=dS)
+    gen = torch.Generator("cuda").manual_seed(2)
+    off = oracle.gdelta_bwd(*(moved(t, gen) for t in x), moved(do, gen), state=moved(S0, gen), dstate=moved(dS, gen))
+    torch.cuda.synchronize()
+    for name, a, b, c, bound, products in list(zip(NAMES, got, ref, off, BOUNDS, (7, 7, 4, 7, 7, 4)))[3:]:
+        assert_close(name, a, b, bound + products * float((c - b).norm() / b.norm()))

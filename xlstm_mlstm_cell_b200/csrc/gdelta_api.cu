@@ -58,7 +58,7 @@ size_t plan(char *base, const Args &a, bool backward, Workspace *w)
         w->P = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
     }
     if (backward) {
-        if (tc && a.DK <= 64) w->GL = reinterpret_cast<uint8_t *>(take(8192 * chunks));
+        if (tc) w->GL = reinterpret_cast<uint8_t *>(take(8192 * chunks));
         w->KK = reinterpret_cast<float *>(take(sizeof(float) * 4096 * chunks));
         w->SC = reinterpret_cast<float *>(take(sizeof(float) * a.DK * a.DV * chunks));
         w->DSC = reinterpret_cast<float *>(take(sizeof(float) * a.DK * a.DV * chunks));

@@ -34,7 +34,7 @@ struct Workspace {
     float2 *GB;            // tensor-core path: [BHV][NC][64] e^a, and beta e^{a_64 - a}
     uint8_t *TG;           // tensor-core path: [BHV][NC] blocks of 32 KB, T - I and G as bf16 parts
     uint8_t *TL;           // tensor-core path: [BHV][NC] blocks of 8 KB, the third part of T - I
-    uint8_t *GL;           // the same of G, the backward with DK <= 64 only
+    uint8_t *GL;           // the same of G, the backward only
     // the backward
     float *SC, *DSC;       // [BHV][NC][DK][DV] states at the chunks' starts, gradients at their ends
     float *E, *DV;         // [BHV][NC][64][DV]

@@ -15,11 +15,11 @@
 // Operands.  K and Q are stacked in shared memory, 64 rows each, so that one M = 128 MMA serves both;
 // the same tile, read MN-major, is the A operand of the state's update.  The fp32 operands S, Y and the
 // state update's enter as three bf16 parts each, which hold all 24 bits, side by side along N: one MMA
-// reads A once for all three, and the epilogue adds the parts' columns.  T - I enters as three parts where the state
-// or E come of it: two (value and rounding residue, 2.5e-6 of the correction) leave the state of slowly forgetting gates
-// 5.5e-7 off where fp32 arithmetic is 1.6e-7, and that of a key that repeats, whose sums nearly cancel, 3e-5 off where
-// it is 5e-7.  Forward the third part costs 0.26 us a chunk of 2.1 (its four MMAs a chain).  G enters as two, which
-// only the bf16 o sees; reverse T - I as two as well, and G as three where DK is at most 64.  K, Q, dO are exact.
+// reads A once for all three, and the epilogue adds the parts' columns.  T - I and, backwards, G enter as three parts
+// too, each the rounding of what is left; forward G as two, which only the bf16 o sees.  With two parts (2.5e-6 of the
+// correction they carry) the state of slowly forgetting gates was 5.5e-7 off where fp32 arithmetic is 1.6e-7, that of a
+// key that repeats, whose sums nearly cancel, 3e-5 where it is 5e-7, and there dbeta 1e-4 where it is 5e-6.  The third
+// parts cost 0.26 us a chunk forward and 0.6 reverse (four and eight MMAs a chain).  K, Q, dO are exact.
 // Without its unit diagonal T leaves Y itself out of the MMA: the threads that formed Y in fp32 add it to the result.
 // The fp32 state stays in the epilogue threads' registers, a row (key element) of 16 columns
 // each, and takes the update with fp32 additions.
@@ -354,27 +354,22 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         const float2 gp = f2_unpack(acc[r >> 1][e]);
                         y[e] = part ? scale * (r & 1 ? gp.y : gp.x) : i0 + r == c0 + e ? 0.f : t[e];
                     }
-                    uint32_t hi[2], lo[2];
+                    uint32_t cut[3][2];   // each part the rounding of what is left
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        hi[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-                        lo[e] = pack_bf16(y[2 * e] - __uint_as_float(hi[e] << 16),
-                                          y[2 * e + 1] - __uint_as_float(hi[e] & 0xffff0000u));
-                    }
-                    const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
-                    *reinterpret_cast<uint2 *>(tg + off) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(lo[0], lo[1]);
-                    if (part == 0 || (BACKWARD && w.GL)) {   // the third part of T - I, and the backward's of G where there is room
-                        float z[4];
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t h = hi[e >> 1], l = lo[e >> 1];
-                            z[e] = (y[e] - __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16)) -
-                                   __uint_as_float(e & 1 ? l & 0xffff0000u : l << 16);
+                        for (int q = 0; q < 3; ++q) {
+                            const uint32_t u = pack_bf16(y[2 * e], y[2 * e + 1]);
+                            cut[q][e] = u;
+                            y[2 * e] -= __uint_as_float(u << 16);
+                            y[2 * e + 1] -= __uint_as_float(u & 0xffff0000u);
                         }
+                    const uint32_t off = sw128_offset(64 * part + i0 + r, c0, 128);
+                    *reinterpret_cast<uint2 *>(tg + off) = make_uint2(cut[0][0], cut[0][1]);
+                    *reinterpret_cast<uint2 *>(tg + 16384 + off) = make_uint2(cut[1][0], cut[1][1]);
+                    if (part == 0 || BACKWARD)   // the third part of T - I, and the backward's of G
                         *reinterpret_cast<uint2 *>((part ? w.GL : w.TL) + ch * 8192 + sw128_offset(i0 + r, c0, 64)) =
-                            make_uint2(pack_bf16(z[0], z[1]), pack_bf16(z[2], z[3]));
-                    }
+                            make_uint2(cut[2][0], cut[2][1]);
                 }
             }
             __syncthreads();
@@ -411,14 +406,14 @@ struct Walk {
     static constexpr int STAGES = 2;
     // A stage: [K; Q] as one or two blocks of 64 columns, then [T - I; G] values and residues, 16 KB each; forward
     // also the third part of T - I, with zeros in G's rows.  With 64 columns a CTA there is room for T - I and G
-    // only once: the next chunk's come behind this one's second product with them (single).  KEEP has
+    // only once: the next chunk's come behind this one's second product with them (single).  Reverse the third parts of
+    // T - I and G have one place likewise.  KEEP has
     // no use for Q and G, whose lanes' sums stay unread: K alone, and three parts of T - I, 8 KB each; the MMAs' rows
-    // 64..127 are then whatever follows, and so are the state's rows from 64 on with one block.  Reverse, a stage of
-    // one block has room for G's third part.
+    // 64..127 are then whatever follows, and so are the state's rows from 64 on with one block.
     static constexpr uint32_t KROWS = MODE == KEEP ? 64 : 128, KB = KROWS * 128, KBLK = KS / 4;
-    static constexpr bool G3 = MODE == REVERSE && KS == 4, SINGLE = MODE == FORWARD && CW == 32;
+    static constexpr bool SINGLE = MODE == FORWARD && CW == 32;
     static constexpr uint32_t KQ = KBLK * KB;
-    static constexpr uint32_t TLOAD = (MODE == KEEP ? 24576 : 32768) + (MODE == FORWARD || G3 ? 8192 : 0);
+    static constexpr uint32_t TLOAD = MODE == KEEP ? 24576 : MODE == FORWARD ? 40960 : 32768;
     static constexpr uint32_t TSIZE = TLOAD + (MODE == FORWARD ? 8192 : 0);
     static constexpr uint32_t STAGE = KQ + (SINGLE ? 0 : TSIZE);
     static constexpr uint32_t TOFF = SINGLE ? STAGES * STAGE : KQ;   // of a stage's, or of the only one
@@ -426,9 +421,10 @@ struct Walk {
     static constexpr uint32_t SP = STAGES * STAGE + (SINGLE ? TSIZE : 0);   // per chain: S parts, 128 rows
     static constexpr uint32_t YN = SP + NCH * BLOCKS * 16384;   // per chain: Y parts, then the update's, a row per token
     static constexpr uint32_t YROWS = MODE == REVERSE ? 128 : 64;   // (reverse: K's tokens, then Q's)
-    static constexpr uint32_t DO = YN + NCH * BLOCKS * YROWS * 128; // reverse: dO, 64 rows, the chains side by side
+    static constexpr uint32_t DO = 3 * CW / 8;             // reverse: dO, 64 rows, in the 16-byte chunks behind Y's parts
+    static constexpr uint32_t T3 = YN + NCH * BLOCKS * YROWS * 128;   // reverse: the third parts of T - I and G
     // the backward: an epilogue warp's 32 rows of fp32 results on their way out
-    static constexpr uint32_t OUT = DO + (MODE == REVERSE ? 8192 : 0);
+    static constexpr uint32_t OUT = T3 + (MODE == REVERSE ? 16384 : 0);
     static constexpr uint32_t BAR = OUT + (MODE == FORWARD ? 0 : NCH * EPI * 2048);
     static constexpr uint32_t NBAR = 2 * STAGES + 7 * NCH + 2;
     static constexpr uint32_t TOTAL = BAR + NBAR * 8 + 16 + 1024;
@@ -456,7 +452,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                const __grid_constant__ CUtensorMap tm_s, const __grid_constant__ CUtensorMap tm_t, const WalkParams p)
 {
     using W = Walk<CW, KS, MODE>;
-    static_assert(MODE != REVERSE || CW == 16, "dO of both chains in one block of columns");
+    static_assert(MODE != REVERSE || CW == 16, "Y's parts leave room for dO");
     constexpr int NST = W::STAGES, NCH = W::NCH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -464,7 +460,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // per chain: S, Y and N written by the epilogue; X, [E; F] and D finished by the MMAs
     uint64_t *full = bars, *empty = bars + NST, *s_ready = bars + 2 * NST, *x_done = s_ready + NCH, *y_ready = x_done + NCH,
              *e_done = y_ready + NCH, *n_ready = e_done + NCH, *d_done = n_ready + NCH, *o_ready = d_done + NCH,
-             *t_full = o_ready + NCH, *t_empty = t_full + 1;   // T - I and G where they have one place
+             *t_full = o_ready + NCH, *t_empty = t_full + 1;   // T - I and G, or their third parts, with one place
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + W::NBAR), *abort_flag = tmem_slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bhv = blockIdx.y, b = bhv / p.NHV, bh = b * p.NH + (bhv % p.NHV) / (p.NHV / p.NH);
@@ -535,13 +531,23 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tt = smem + W::TOFF;
                     mbar_arrive_expect_tx(t_full, W::TLOAD);
                 }
+                if (MODE == REVERSE) {
+                    bulk_prefetch(p.w.TL + ch * 8192, 8192);
+                    bulk_prefetch(p.w.GL + ch * 8192, 8192);
+                }
                 if (MODE == KEEP) {
                     bulk_load(tt, p.w.TG + ch * 32768, 8192, tbar);
                     bulk_load(tt + 8192, p.w.TG + ch * 32768 + 16384, 8192, tbar);
                     bulk_load(tt + 16384, p.w.TL + ch * 8192, 8192, tbar);
                 } else {
                     bulk_load(tt, p.w.TG + ch * 32768, 32768, tbar);
-                    if (MODE == FORWARD || W::G3) bulk_load(tt + 32768, (W::G3 ? p.w.GL : p.w.TL) + ch * 8192, 8192, tbar);
+                    if (MODE == FORWARD) bulk_load(tt + 32768, p.w.TL + ch * 8192, 8192, tbar);
+                }
+                if (MODE == REVERSE) {
+                    if (c > 0 && !mbar_wait(t_empty, (uint32_t)(c - 1) & 1u, wc)) break;
+                    mbar_arrive_expect_tx(t_full, 16384);
+                    bulk_load(smem + W::T3, p.w.TL + ch * 8192, 8192, t_full);
+                    bulk_load(smem + W::T3 + 8192, p.w.GL + ch * 8192, 8192, t_full);
                 }
             }
         }
@@ -556,7 +562,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             constexpr uint32_t IDG0 = idesc_bf16(128, CW, 0, 1), RES = MODE == KEEP ? 512 : 1024;
             constexpr uint32_t IDTM = idesc_bf16(128, 2 * CW, 1, 1), IDG = idesc_bf16(128, CW, 1, 1);
             const uint64_t atm = smem_desc(smem_u32(smem) + W::TOFF, 8192, 1024);
-            const uint64_t bo = MODE == REVERSE ? smem_desc(smem_u32(smem + W::DO), 8192, 1024) : 0;
+            const uint64_t at3 = MODE == REVERSE ? smem_desc(smem_u32(smem + W::T3), 8192, 1024) : 0;
             const uint64_t bs = smem_desc(smem_u32(smem + W::SP), 16384, 1024);
             const uint64_t by = smem_desc(smem_u32(smem + W::YN), W::YROWS * 128, 1024);
             const uint64_t ak = smem_desc(smem_u32(smem), 16, 1024), at = smem_desc(smem_u32(smem) + W::TOFF, 16, 1024);
@@ -579,17 +585,17 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 // reverse: G^T dO, and the update's share of Q's tokens; neither waits for the state
                 auto issue_q = [&](int h) {
                     if (!(ok = ok && mbar_wait(&o_ready[h], ph, wc))) return;
+                    if (h == 0 && !(ok = ok && mbar_wait(t_full, ph, wc))) return;
                     tc_fence_after();
-                    if (W::G3) {
+                    const uint64_t bo = by + (uint64_t)(h * BY + W::DO);
+                    // smallest first; G's rows lie 8 KB into each part's tile
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_ss(tmem + h * W::TCH + W::TG, atm + to + (uint64_t)(2048 + k * 128),
-                                   bo + (uint64_t)(h * CW / 8 + k * 128), IDG, k > 0);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        mma_ss(tmem + h * W::TCH + W::TG, at3 + (uint64_t)(512 + k * 128), bo + (uint64_t)(k * 128), IDG, k > 0);
 #pragma unroll
-                    for (int k = 7; k >= 0; --k)   // G's rows lie 8 KB into the values' tile, and 16 KB further its residues'
+                    for (int k = 7; k >= 0; --k)   // the values' tile, and 16 KB further the residues'
                         mma_ss(tmem + h * W::TCH + W::TG, atm + to + (uint64_t)(512 + (k >> 2) * 1024 + (k & 3) * 128),
-                               bo + (uint64_t)(h * CW / 8 + (k & 3) * 128), IDG, W::G3 || k < 7);
+                               bo + (uint64_t)((k & 3) * 128), IDG, 1);
 #pragma unroll
                     for (int k = 4; k < 8; ++k)
                         mma_ss(tmem + h * W::TCH + W::TD, ad + so + (uint64_t)(k * 128), by + (uint64_t)(h * BY + k * 128), IDD, k > 4);
@@ -599,24 +605,30 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (!(ok = ok && mbar_wait(&y_ready[h], ph, wc))) return;
                     tc_fence_after();
                     const uint32_t de = tmem + h * W::TCH + W::TE;
-                    // the smallest products first: an MMA cuts off at the size of the sum it adds to.  The residues of
-                    // T - I and G, without Y's third part (but for the first, which writes all columns)
+                    // An MMA cuts off at the size of the sum it adds to, so products of one size share columns: the values
+                    // of T - I and G with Y's three parts; their residues with Y's first two go to the second and third
+                    // of these, the third part of T - I with Y's first to the third.  The tokens nearest to the diagonal
+                    // come last
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(de, MODE == REVERSE ? atm + to + (uint64_t)(1024 + k * 128) : at + to + (uint64_t)(RES + k * 2),
-                               by + (uint64_t)(h * BY + k * 128),
-                               MODE == REVERSE ? (k ? IDTM : IDD) : (k ? IDM : IDX), k > 0);
-                    if (MODE != REVERSE) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)   // the third part of T - I with Y's first
-                            mma_ss(de, at + to + (uint64_t)(2 * RES + k * 2), by + (uint64_t)(h * BY + k * 128), IDG0, 1);
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = MODE == REVERSE ? 3 - i : i;
+                        mma_ss(de, MODE == REVERSE ? atm + to + (uint64_t)(k * 128) : at + to + (uint64_t)(k * 2),
+                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDD : IDX, i > 0);
                     }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ss(de, MODE == REVERSE ? atm + to + (uint64_t)(k * 128) : at + to + (uint64_t)(k * 2),
-                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDD : IDX, 1);
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = MODE == REVERSE ? 3 - i : i;
+                        mma_ss(de + CW, MODE == REVERSE ? atm + to + (uint64_t)(1024 + k * 128) : at + to + (uint64_t)(RES + k * 2),
+                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDTM : IDM, 1);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = MODE == REVERSE ? 3 - i : i;
+                        mma_ss(de + 2 * CW, MODE == REVERSE ? at3 + (uint64_t)(k * 128) : at + to + (uint64_t)(2 * RES + k * 2),
+                               by + (uint64_t)(h * BY + k * 128), MODE == REVERSE ? IDG : IDG0, 1);
+                    }
                     mma_commit(&e_done[h]);
-                    if (W::SINGLE && h == NCH - 1) mma_commit(t_empty);
+                    if ((W::SINGLE || MODE == REVERSE) && h == NCH - 1) mma_commit(t_empty);
                 };
                 auto issue_d = [&](int h) {
                     if (!(ok = ok && mbar_wait(&n_ready[h], ph, wc))) return;
@@ -701,7 +713,7 @@ walk_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             uint64_t x[8], y[8];
             if (MODE == REVERSE && !krow) {   // dO itself, and scale e^a dO behind the K tokens' rows
 #pragma unroll
-                for (int e = 0; e < 2; ++e) *reinterpret_cast<uint4 *>(smem + W::DO + sw128_chunk(t, h * (CW / 8) + cg * 2 + e, 64)) = vr[e];
+                for (int e = 0; e < 2; ++e) *reinterpret_cast<uint4 *>(yn + sw128_chunk(t, W::DO + e, W::YROWS)) = vr[e];
                 const uint64_t f = f2_pack(p.scale * ea, p.scale * ea);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = f2_mul(f, f2_from_bf16x2((&vr[e >> 2].x)[e & 3]));

@@ -31,6 +31,11 @@
  * The recurrence is stable for keys of norm at most about one with beta in [0, 2];
  * nothing here normalizes them (qknorm.h does).
  *
+ * Real tokens have to be finite (g may be -inf: a full reset).  Over sequences the zeros of a chunk's
+ * triangular matrices meet every token of the chunk, so an infinity or NaN in one makes NaN of the
+ * outputs of all tokens of its chunk of 64, the earlier ones among them, and of everything behind it; with
+ * gradients, of everything.  Other items, and heads that read neither its keys nor its values, are not touched.
+ *
  * `lengths` (device int32 [B], or NULL for S everywhere): of item b only the first
  * lengths[b] tokens (clamped to [0, S]) are part of the sequence.  The rows behind
  * are not used, whatever they hold, and the state is the one after the last real

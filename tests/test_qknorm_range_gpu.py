@@ -64,3 +64,17 @@ def test_a_zero_vector_among_others():
     x[:, 4] = 0
     dx, rx = check(x, dy, w, inv, "l2", 1e-30)
     assert_close("dx of the others", dx[:, :4], rx[:, :4], G32)
+
+
+def test_given_workspace():
+    """As large as the query says, whatever it held; one byte less is refused."""
+    x, dy, w, inv = make(64, 32, "bf16", 1.0, 5)
+    kw = dict(q_weight=w, k_weight=w, inv_freq=inv)
+    n = binding.qknorm_bwd_workspace_size(2, 9, 3, 3, 64)
+    ref = binding.qknorm_bwd(dy, dy, x, x, **kw)
+    got = binding.qknorm_bwd(dy, dy, x, x, workspace=torch.full((n,), 0xff, dtype=torch.uint8, device="cuda"), **kw)
+    for a, b in zip(ref, got):
+        assert torch.equal(a, b)
+    with pytest.raises(binding.MlstmError):
+        binding.qknorm_bwd(dy, dy, x, x, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"), **kw)
+    assert binding.qknorm_bwd_workspace_size(2, 9, 3, 3, 12) == 0

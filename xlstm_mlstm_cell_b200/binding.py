@@ -571,6 +571,11 @@ def _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions):
     return dt, B, S, NHQ, NHK, D, RD, QKNORM_KINDS[norm], index
 
 
+def qknorm_bwd_workspace_size(B, S, NHQ, NHK, D) -> int:
+    """Workspace bytes of a qknorm_bwd with weights (0: unsupported)."""
+    return int(load().qknorm_bwd_workspace_size(B, S, NHQ, NHK, D))
+
+
 def _strides(t):
     b, s, h, _ = t.stride()
     return _Strides(b, s, h)
@@ -608,7 +613,8 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm: str = "
                inv_freq=None, positions=None, interleaved: bool = False, out=None, workspace=None, stream=None):
     """qknorm_bwd: the gradients ``(dq, dk, dq_weight, dk_weight)`` of qknorm_fwd's inputs from those of its
     outputs (weight gradients None where the weight is).  ``out`` may give dq ``[B, S, NHQ, D]`` and dk to
-    write into, such as slices of a fused projection's gradient (views that share no element)."""
+    write into, such as slices of a fused projection's gradient (views that share no element), ``workspace`` the
+    bytes that qknorm_bwd_workspace_size names."""
     lib = load()
     dt, B, S, NHQ, NHK, D, RD, kind, index = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
     _need("dq_out", dq_out, (B, NHQ, S, D), q.dtype, index)

@@ -28,8 +28,8 @@ struct Args {
 struct Workspace {
     uint32_t *status;      // bounded-wait status word (0 = fine)
     int NC;
-    float2 *A;             // [BHV][NC][64] cumulative log gate of the chunk as value and residue (tensor-core
-                           // path: in units of log 2)
+    float2 *A;             // [BHV][NC][64] cumulative log gate of the chunk as value and residue: natural logarithms,
+                           // but on the tensor-core path, whose kernels alone read them there, binary ones
     float *T, *P, *KK;     // [BHV][NC][64][64] (row i, column j); KK the backward only
     float2 *GB;            // tensor-core path: [BHV][NC][64] e^a, and beta e^{a_64 - a}
     uint8_t *TG;           // tensor-core path: [BHV][NC] blocks of 32 KB, T - I and G as bf16 parts

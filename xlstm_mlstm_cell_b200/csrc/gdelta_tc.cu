@@ -178,7 +178,7 @@ MLSTM_DEVINL void join(float *mr, float *mc, int at, int tid, bool on, Sync sync
 // The inverse (diagonal blocks of 16 by substitution,
 // then joins, as invert64) and P diag(beta) T run on the CUDA cores in fp32 from shared memory, 4 x 4
 // tiles fed by two 16-byte loads per reduction step; four CTAs an SM overlap their short serial parts.
-// 8192 chunks of 128 key elements in pairs of value heads take 224 us, 1.5 us a chunk's SM: half of the
+// 8192 chunks of 128 key elements in pairs of value heads take 235 us, 4.2 us of an SM each: half of the
 // shared-memory rate, the rest barriers between the joins.  G on the tensor cores needs P and T in three parts each
 // (two lose 1e-4 of beta's gradient where keys repeat) and took 305 us with their splitting; CTAs of 64 threads
 // 222 to 300 us.
@@ -391,9 +391,9 @@ prep_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
 // A CTA runs two chains side by side, CW value columns each, on the same K, Q, T and G tiles: while the
 // epilogue warps of one pass over an accumulator, the MMAs of the other run.  What bounds a walk is that chain: 2.4 us
-// a chunk at CW 16 (32 heads of 16384 tokens, 128 x 128: 605 us, 128 CTAs); with the states
-// and E kept 2.6 us, at CW 32 4.6 us (4 x 16 heads of 4096 tokens: 292 us, against 338 in two rounds of CTAs at CW
-// 16); reverse 3.2 us.  The tensor pipe is busy a quarter of it, the rest are the epilogues' passes from TMEM over registers to shared memory and the
+// a chunk at CW 16 (32 heads of 16384 tokens, 128 x 128: 615 us, 128 CTAs), 4.3 us at CW 32; with the states
+// and E kept 2.7 us, at CW 32 4.6 us (4 x 16 heads of 4096 tokens: 295 us, against 338 in two rounds of CTAs at CW
+// 16); reverse 3.9 us.  The tensor pipe is busy a quarter of it, the rest are the epilogues' passes from TMEM over registers to shared memory and the
 // waits between the two.  One chain of 32 columns, three or four chains, or 8 columns a thread were no faster.
 enum Mode { FORWARD, KEEP, REVERSE };   // KEEP: the forward walk again, for the backward: states and E, no outputs
 
@@ -858,7 +858,8 @@ cudaError_t launch_walk_tc(const Args &a, const Workspace &w, const Maps &qk, co
                             !tcfwd::make_map_f32(&m[3], MODE == KEEP ? w.E : w.DV, a.DV, 64, a.B * a.NHV * w.NC)))
         return cudaErrorUnknown;
     // While the GPU has SMs for it a CTA takes 32 columns; 64 take fewer CTAs than twice the time (the epilogue
-    // warps of the K tokens, two of the SM's four schedulers, are what a chunk then waits for).  The reverse
+    // warps of the K tokens, two of the SM's four schedulers, are what a chunk then waits for): a forward call of 192,
+    // 256 and 512 CTAs of 32 columns took 405, 427 (4096 tokens) and 378 us (2048), half as many of 64 361, 382 and 331.  The reverse
     // walk always takes 32: Q's share of the update and the results' way out take the shared memory
     const bool narrow = MODE == REVERSE || (long long)a.B * a.NHV * ((a.DV + 31) / 32) <= 148;
     if constexpr (MODE != REVERSE)

@@ -291,7 +291,7 @@ MLSTM_DEVINL void one_side(const Params &p, const Side &sd, const Place<VEC, SPA
             s += has[n] ? f2_unpack(s2).x + f2_unpack(s2).y : 0.f;
             if (BWD) xd += has[n] ? f2_unpack(xd2).x + f2_unpack(xd2).y : 0.f;
         }
-        if (!BWD && NU == 1 && !INTER) {   // the shortest body: 61 us, 63 with the steps unrolled; 72 elements 88 and 72 us
+        if (!BWD && NU == 1 && !INTER) {   // the shortest body: 61 us, 63 with the steps unrolled
             for (int o = p.GL / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
         } else {
 #pragma unroll

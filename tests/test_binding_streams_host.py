@@ -7,7 +7,6 @@ and an output has to be recorded on the current stream, where the caller uses it
 """
 from __future__ import annotations
 
-import contextlib
 import types
 
 import pytest
@@ -15,15 +14,22 @@ import torch
 
 from xlstm_mlstm_cell_b200 import binding
 
-GIVEN = types.SimpleNamespace(cuda_stream=0x51, device=torch.device("cuda", 0), device_index=0, name="given")
-CALLER = types.SimpleNamespace(cuda_stream=0x52, device=torch.device("cuda", 0), device_index=0, name="caller")
+GIVEN, CALLER, FOREIGN = (types.SimpleNamespace(cuda_stream=0x5100 + i, device="device %d" % i, device_index=i)
+                          for i in (-1, -1, 3))   # the stand-ins' tensors are on the CPU, device -1
+CALLER.cuda_stream = 0x5200
 
 
 class Library:
-    """Every entry point succeeds; every size is 512 bytes."""
+    """Every entry point succeeds and notes the streams among its arguments; every size is 512 bytes."""
+
+    def __init__(self):
+        self.streams = []
 
     def __getattr__(self, name):
-        return lambda *a: 512 if name.endswith("_size") else 0
+        def call(*a):
+            self.streams += [x for x in a if type(x) is int and x in (GIVEN.cuda_stream, CALLER.cuda_stream)]
+            return 512 if name.endswith("_size") else 0
+        return call
 
 
 @pytest.fixture
@@ -31,30 +37,30 @@ def notes(monkeypatch):
     """Allocations as (tensor, stream current at that moment) and the streams each was recorded on."""
     made, recorded, current = [], {}, [CALLER]
 
-    @contextlib.contextmanager
-    def stream(s):
-        current.append(s)
-        yield
-        current.pop()
+    def set_stream(s):
+        current[0] = s
 
     def noting(make):
         def wrapped(*a, **kw):
             kw.pop("device", None)
             t = make(*a, **kw)
-            made.append((t, current[-1]))
+            made.append((t, current[0]))
             return t
         return wrapped
 
     for name in ("empty", "empty_like", "zeros"):
         monkeypatch.setattr(torch, name, noting(getattr(torch, name)))
-    monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[-1])
+    monkeypatch.setattr(torch.cuda, "set_stream", set_stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: current[0])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.setdefault(id(t), []).append(s))
-    monkeypatch.setattr(binding, "load", lambda *a: Library())
+    lib = Library()
+    monkeypatch.setattr(binding, "load", lambda *a: lib)
     monkeypatch.setattr(binding, "_cuda_index", lambda t: t.get_device())
-    monkeypatch.setattr(binding, "_stream", lambda s: None)
-    monkeypatch.setattr(binding, "_on", lambda index, stream, call: call(0))
-    return made, recorded
+    monkeypatch.setattr(binding, "_stream", lambda *a: current[0].cuda_stream)
+    monkeypatch.setattr(binding, "_on", lambda index, call: call(current[0].cuda_stream))
+    yield made, recorded, lib.streams
+    assert current == [CALLER], "the current stream is not what it was"
 
 
 def rand(*shape):
@@ -102,9 +108,9 @@ CELLS = {
 
 
 def check_given_stream(call, tensors, notes):
-    made, recorded = notes
+    made, recorded, launched = notes
     call(stream=GIVEN)
-    assert len(made) == tensors
+    assert len(made) == tensors and launched == [GIVEN.cuda_stream]
     for t, where in made:
         assert where is GIVEN, "allocated on the current stream, used on the given one"
         assert recorded.get(id(t)) == (None if t.dtype == torch.uint8 else [CALLER])   # workspaces are bytes
@@ -124,7 +130,16 @@ def test_a_given_streams_cell_allocates_from_that_stream(name, notes):
 
 @pytest.mark.parametrize("name", sorted(OPERATORS) + sorted(CELLS))
 def test_a_call_on_the_current_stream_allocates_there(name, notes):
-    made, recorded = notes
+    made, recorded, launched = notes
     call, tensors = {**OPERATORS, **CELLS}[name]
     call()
     assert len(made) == tensors and all(where is CALLER for _, where in made) and not recorded
+    assert launched == [CALLER.cuda_stream]
+
+
+@pytest.mark.parametrize("name", sorted(OPERATORS) + sorted(CELLS))
+def test_a_stream_of_another_device_is_refused(name, notes):
+    made, _, launched = notes
+    with pytest.raises(ValueError, match="stream"):
+        {**OPERATORS, **CELLS}[name][0](stream=FOREIGN)
+    assert not made and not launched

@@ -4,7 +4,8 @@ The functions take torch tensors that already live on the GPU, pass their
 device pointers, sizes and the current CUDA stream to the C ABI declared in
 ``include/*.h``, and raise ``MlstmError`` on a non-zero status.  Every step
 of the computation runs in the library's CUDA kernels; there is no other code
-path.  If the library cannot be loaded the import of the functions fails
+path.  A call runs on the current stream, or as one on ``stream`` where that is
+given.  If the library cannot be loaded the import of the functions fails
 loudly (``load()`` raises).
 """
 from __future__ import annotations
@@ -111,7 +112,7 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+def _stream(stream=None):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -121,26 +122,35 @@ def _check(fn, status):
         raise MlstmError(fn, status, _lib)
 
 
-def _scratch(n, device, stream):
-    """A workspace for one call.  With a stream of the caller's it comes from that stream's memory: a block of the
-    current stream's may still be in use by work queued there, for which the call's kernels do not wait."""
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
+def _on_stream(stream, fn, tensor, *args, **kwargs):
+    """``fn(tensor, *args, **kwargs)`` as a call on ``stream``.
+
+    The stream is the current one meanwhile, so that what the call allocates comes from its memory: a block of the
+    caller's stream could still be in use by work queued there, for which the call's kernels do not wait.  The results
+    are recorded on the caller's stream, where it goes on to use them, so that a block is not handed on before that is
+    done either.
+    """
+    if tensor.get_device() != stream.device_index:
+        raise ValueError("the tensors are on %s, the stream on %s" % (tensor.device, stream.device))
+    device, caller = torch._C._cuda_getDevice(), torch.cuda.current_stream(stream.device_index)
+    torch.cuda.set_stream(stream)
+    try:
+        out = fn(tensor, *args, **kwargs)
+    finally:
+        torch.cuda.set_stream(caller)
+        if device != stream.device_index:   # selecting a stream selects its device
+            torch.cuda.set_device(device)
+    if caller != stream:
+        _record(out, caller)
+    return out
 
 
-def _new(stream, make):
-    """``make()``, an output that a call allocates itself: from the memory of a given stream, as a workspace is, and
-    recorded on the current one, where the caller goes on to use it, so that its block is not handed on before that
-    is done either."""
-    if stream is None:
-        return make()
-    caller = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        t = make()
-    t.record_stream(caller)
-    return t
+def _record(out, stream):
+    if isinstance(out, torch.Tensor):
+        out.record_stream(stream)
+    elif out is not None:
+        for x in out:
+            _record(x, stream)
 
 
 def workspace_size(B, NH, S, DHQK, DHV, chunk, dtype) -> int:
@@ -172,11 +182,11 @@ def fwd_segments(B, NH, S, DHQK, DHV, chunk, dtype) -> int:
     return int(load().mlstm_fwd_segments(B, NH, S, DHQK, DHV, chunk, dt))
 
 
-def alloc_workspace(B, NH, S, DHQK, DHV, chunk, dtype, device="cuda", stream=None) -> torch.Tensor:
+def alloc_workspace(B, NH, S, DHQK, DHV, chunk, dtype, device="cuda") -> torch.Tensor:
     n = workspace_size(B, NH, S, DHQK, DHV, chunk, dtype)
     if n == 0:
         raise MlstmError("mlstm_fwd_workspace_size", 2)
-    return _scratch(n, device, stream)
+    return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 FWD_PHASES = 4
@@ -192,24 +202,27 @@ def fwd(q, k, v, igate, fgate, ogate=None, chunk: int = 64, h_out=None, C_final=
     mlstm_fwd_profiled, which records them around its phases on the stream; ``events[FWD_PHASES
     - 1]`` completes once the final state is written.
     """
+    if stream is not None:
+        return _on_stream(stream, fwd, q, k, v, igate, fgate, ogate, chunk, h_out, C_final, n_final, m_final,
+                          workspace, return_state, events=events, state=state)
     lib = load()
     B, NH, S, DHQK = q.shape
     DHV = v.shape[-1]
     dt = _dt(q)
     if h_out is None:
-        h_out = _new(stream, lambda: torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device))
+        h_out = torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device)
     if return_state:
         if C_final is None:
-            C_final = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device))
+            C_final = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device)
         if n_final is None:
-            n_final = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device))
+            n_final = torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device)
         if m_final is None:
-            m_final = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=q.device))
+            m_final = torch.empty((B, NH), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, q.dtype, q.device, stream)
+        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, q.dtype, q.device)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _ptr(ogate), dt, B, NH, S, DHQK, DHV, chunk,
             _ptr(h_out), _ptr(C_final), _ptr(n_final), _ptr(m_final), _ptr(workspace), workspace.numel(),
-            _stream(stream))
+            _stream())
     if state is not None:
         assert events is None
         C0, n0, m0 = state
@@ -242,47 +255,53 @@ def bwd(q, k, v, igate, fgate, ogate, dh, chunk: int = 64, workspace=None, strea
     """mlstm_bwd on device tensors: gradients of sum(dh * h) for the forward pass from the zero
     state.  Returns ``(dq, dk, dv, digate, dfgate, dogate)`` (dogate None without an output gate);
     ``out`` may give those six tensors to write into."""
+    if stream is not None:
+        return _on_stream(stream, bwd, q, k, v, igate, fgate, ogate, dh, chunk, workspace, out=out)
     lib = load()
     B, NH, S, DHQK = q.shape
     DHV = v.shape[-1]
     dt = _dt(q)
     if out is None:
-        out = tuple(None if x is None else _new(stream, lambda: torch.empty_like(x))
-                    for x in (q, k, v, igate, fgate, ogate))
+        out = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(igate),
+               torch.empty_like(fgate), None if ogate is None else torch.empty_like(ogate))
     dq, dk, dv, dig, dfg, dog = out
     if workspace is None:
         n = bwd_workspace_size(B, NH, S, DHQK, DHV, chunk, q.dtype)
         if n == 0:
             raise MlstmError("mlstm_bwd_workspace_size", 2)
-        workspace = _scratch(n, q.device, stream)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     _check("mlstm_bwd", lib.mlstm_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _ptr(ogate), _ptr(dh), dt,
                                       B, NH, S, DHQK, DHV, chunk, _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dig), _ptr(dfg),
-                                      _ptr(dog), _ptr(workspace), workspace.numel(), _stream(stream)))
+                                      _ptr(dog), _ptr(workspace), workspace.numel(), _stream()))
     return dq, dk, dv, dig, dfg, dog
 
 
 def fwd_final_state(k, v, igate, fgate, chunk: int = 64, workspace=None, stream=None):
     """mlstm_fwd_final_state: ``(C, n, m)`` of the sequence from the zero state, no outputs."""
+    if stream is not None:
+        return _on_stream(stream, fwd_final_state, k, v, igate, fgate, chunk, workspace)
     lib = load()
     B, NH, S, DHQK = k.shape
     DHV = v.shape[-1]
-    C = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=k.device))
-    n = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=k.device))
-    m = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=k.device))
+    C = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=k.device)
+    n = torch.empty((B, NH, DHQK), dtype=torch.float32, device=k.device)
+    m = torch.empty((B, NH), dtype=torch.float32, device=k.device)
     if workspace is None:
-        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, k.dtype, k.device, stream)
+        workspace = alloc_workspace(B, NH, S, DHQK, DHV, chunk, k.dtype, k.device)
     _check("mlstm_fwd_final_state",
            lib.mlstm_fwd_final_state(_ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _dt(k), B, NH, S, DHQK, DHV, chunk,
-                                     _ptr(C), _ptr(n), _ptr(m), _ptr(workspace), workspace.numel(), _stream(stream)))
+                                     _ptr(C), _ptr(n), _ptr(m), _ptr(workspace), workspace.numel(), _stream()))
     return C, n, m
 
 
 def log_decay_sum(fgate, stream=None):
     """mlstm_log_decay_sum: per (b, h) the sum over tokens of logsigmoid(f~), ``[B, NH]``."""
+    if stream is not None:
+        return _on_stream(stream, log_decay_sum, fgate)
     lib = load()
     B, NH, S = fgate.shape
-    g = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=fgate.device))
-    _check("mlstm_log_decay_sum", lib.mlstm_log_decay_sum(_ptr(fgate), B, NH, S, _ptr(g), _stream(stream)))
+    g = torch.empty((B, NH), dtype=torch.float32, device=fgate.device)
+    _check("mlstm_log_decay_sum", lib.mlstm_log_decay_sum(_ptr(fgate), B, NH, S, _ptr(g), _stream()))
     return g
 
 
@@ -290,14 +309,16 @@ def state_prefix(C_parts, n_parts, m_parts, g_parts, rank: int, stream=None):
     """mlstm_state_prefix: the start state ``(C0, n0, m0)`` of slice ``rank`` from the gathered
     summaries ``C_parts [R, B, NH, DHQK, DHV]``, ``n_parts [R, B, NH, DHQK]``, ``m_parts`` and
     ``g_parts [R, B, NH]``."""
+    if stream is not None:
+        return _on_stream(stream, state_prefix, C_parts, n_parts, m_parts, g_parts, rank)
     lib = load()
     R, B, NH, DHQK, DHV = C_parts.shape
-    C0 = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=C_parts.device))
-    n0 = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=C_parts.device))
-    m0 = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=C_parts.device))
+    C0 = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=C_parts.device)
+    n0 = torch.empty((B, NH, DHQK), dtype=torch.float32, device=C_parts.device)
+    m0 = torch.empty((B, NH), dtype=torch.float32, device=C_parts.device)
     _check("mlstm_state_prefix",
            lib.mlstm_state_prefix(_ptr(C_parts), _ptr(n_parts), _ptr(m_parts), _ptr(g_parts), R, rank, B, NH, DHQK,
-                                  DHV, _ptr(C0), _ptr(n0), _ptr(m0), _stream(stream)))
+                                  DHV, _ptr(C0), _ptr(n0), _ptr(m0), _stream()))
     return C0, n0, m0
 
 
@@ -311,20 +332,22 @@ def fwd_noalloc(q, k, v, igate, fgate, ogate=None, chunk: int = 64, h_out=None, 
     For callers that may not allocate device memory for a workspace (the outputs are still
     the caller's).  Returns ``(h, C, n, m)``.
     """
+    if stream is not None:
+        return _on_stream(stream, fwd_noalloc, q, k, v, igate, fgate, ogate, chunk, h_out, C_final, n_final, m_final)
     lib = load()
     B, NH, S, DHQK = q.shape
     DHV = v.shape[-1]
     if h_out is None:
-        h_out = _new(stream, lambda: torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device))
+        h_out = torch.empty((B, NH, S, DHV), dtype=q.dtype, device=q.device)
     if C_final is None:
-        C_final = _new(stream, lambda: torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device))
+        C_final = torch.empty((B, NH, DHQK, DHV), dtype=torch.float32, device=q.device)
     if n_final is None:
-        n_final = _new(stream, lambda: torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device))
+        n_final = torch.empty((B, NH, DHQK), dtype=torch.float32, device=q.device)
     if m_final is None:
-        m_final = _new(stream, lambda: torch.empty((B, NH), dtype=torch.float32, device=q.device))
+        m_final = torch.empty((B, NH), dtype=torch.float32, device=q.device)
     st = lib.mlstm_fwd_noalloc(_ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate), _ptr(ogate), _dt(q), B, NH,
                                S, DHQK, DHV, chunk, _ptr(h_out), _ptr(C_final), _ptr(n_final), _ptr(m_final),
-                               _stream(stream))
+                               _stream())
     _check("mlstm_fwd_noalloc", st)
     return h_out, C_final, n_final, m_final
 
@@ -341,13 +364,15 @@ def fwd_status(workspace, stream=None) -> int:
 
 def step(C, n, m, q, k, v, igate, fgate, ogate=None, h_out=None, stream=None):
     """mlstm_step on device tensors; the state (C, n, m) is updated in place; returns h."""
+    if stream is not None:
+        return _on_stream(stream, step, C, n, m, q, k, v, igate, fgate, ogate, h_out)
     lib = load()
     B, NH, DHQK = q.shape
     DHV = v.shape[-1]
     if h_out is None:
-        h_out = _new(stream, lambda: torch.empty((B, NH, DHV), dtype=q.dtype, device=q.device))
+        h_out = torch.empty((B, NH, DHV), dtype=q.dtype, device=q.device)
     st = lib.mlstm_step(_ptr(C), _ptr(n), _ptr(m), _ptr(q), _ptr(k), _ptr(v), _ptr(igate), _ptr(fgate),
-                        _ptr(ogate), _dt(q), B, NH, DHQK, DHV, _ptr(h_out), _stream(stream))
+                        _ptr(ogate), _dt(q), B, NH, DHQK, DHV, _ptr(h_out), _stream())
     _check("mlstm_step", st)
     return h_out
 
@@ -362,16 +387,17 @@ def slstm_fwd(wx, R, forget: str = "exp", state=None, h_out=None, want_h: bool =
     """
     if forget not in ("exp", "sigmoid"):
         raise ValueError("forget must be 'exp' or 'sigmoid'")
+    if stream is not None:
+        return _on_stream(stream, slstm_fwd, wx, R, forget, state, h_out, want_h, status)
     lib = load()
     B, S, _, NH, DH = wx.shape
     if state is None:
-        zeros = lambda: torch.zeros((B, NH, DH), dtype=torch.float32, device=wx.device)   # noqa: E731 - on the call's stream
-        state = tuple(_new(stream, zeros) for _ in range(4))
+        state = tuple(torch.zeros((B, NH, DH), dtype=torch.float32, device=wx.device) for _ in range(4))
     c, n, m, h = state
     if want_h and h_out is None:
-        h_out = _new(stream, lambda: torch.empty((B, S, NH, DH), dtype=wx.dtype, device=wx.device))
+        h_out = torch.empty((B, S, NH, DH), dtype=wx.dtype, device=wx.device)
     st = lib.slstm_fwd(_ptr(wx), _ptr(R), _dt(wx), B, S, NH, DH, 1 if forget == "sigmoid" else 0, _ptr(c), _ptr(n),
-                       _ptr(m), _ptr(h), _ptr(h_out if want_h else None), _ptr(status), _stream(stream))
+                       _ptr(m), _ptr(h), _ptr(h_out if want_h else None), _ptr(status), _stream())
     _check("slstm_fwd", st)
     return (h_out if want_h else None), (c, n, m, h)
 
@@ -407,11 +433,10 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(index, stream, call):
-    """``call(stream address)`` with the arguments' device as the current one, on ``stream`` or on the
-    device's current stream."""
+def _on(index, call):
+    """``call(stream address)`` with the arguments' device as the current one, on that device's current stream."""
     current = torch._C._cuda_getDevice()
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    s = torch._C._cuda_getCurrentRawStream(index)
     if current == index:
         return call(s)
     torch.cuda.set_device(index)
@@ -450,14 +475,14 @@ def gdelta_workspace_size(B, NH, NHV, S, DK, DV, dtype, backward: bool = False) 
     return int(size(B, NH, NHV, S, DK, DV, dt))
 
 
-def _gdelta_workspace(workspace, sizes, device, index, backward, stream):
+def _gdelta_workspace(workspace, sizes, device, index, backward):
     if workspace is None:
         lib = load()
         fn = "gdelta_bwd_workspace_size" if backward else "gdelta_fwd_workspace_size"
         n = int(getattr(lib, fn)(*sizes))
         if n == 0:
             raise MlstmError(fn, 2, lib)
-        return _scratch(n, device, stream)
+        return torch.empty(n, dtype=torch.uint8, device=device)
     _need("workspace", workspace, workspace.shape, torch.uint8, index)
     return workspace
 
@@ -472,20 +497,23 @@ def gdelta_fwd(q, k, v, g, beta, state=None, lengths=None, scale=None, o_out=Non
     ``lengths`` int32 ``[B]`` the real tokens of each item (None: all); ``scale`` defaults to
     DK ** -0.5.  The state is None with ``return_state=False``.
     """
+    if stream is not None:
+        return _on_stream(stream, gdelta_fwd, q, k, v, g, beta, state, lengths, scale, o_out, state_out,
+                          return_state, workspace)
     lib = load()
     dt, B, NH, NHV, S, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, lengths)
     if state is not None:
         _need("state", state, (B, NHV, DK, DV), torch.float32, index)
     if o_out is None:
-        o_out = _new(stream, lambda: torch.empty_like(v))
+        o_out = torch.empty_like(v)
     else:
         _need("o_out", o_out, v.shape, q.dtype, index)
     if state_out is not None:
         _need("state_out", state_out, (B, NHV, DK, DV), torch.float32, index)
     elif return_state:
-        state_out = _new(stream, lambda: torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device))
-    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, False, stream)
-    _check("gdelta_fwd", _on(index, stream, lambda s: lib.gdelta_fwd(
+        state_out = torch.empty((B, NHV, DK, DV), dtype=torch.float32, device=q.device)
+    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, False)
+    _check("gdelta_fwd", _on(index, lambda s: lib.gdelta_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), dt, B, NH, NHV, S, DK,
         DV, DK ** -0.5 if scale is None else scale, _addr(state), o_out.data_ptr(), _addr(state_out),
         workspace.data_ptr(), workspace.numel(), s)))
@@ -495,14 +523,16 @@ def gdelta_fwd(q, k, v, g, beta, state=None, lengths=None, scale=None, o_out=Non
 def gdelta_step(state, q, k, v, g, beta, scale=None, o_out=None, stream=None):
     """gdelta_step: one token of the gated delta rule; updates ``state`` ``[B, NHV, DK, DV]`` in place
     and returns o ``[B, NHV, DV]``.  q, k ``[B, NH, DK]``, v ``[B, NHV, DV]``, g, beta ``[B, NHV]``."""
+    if stream is not None:
+        return _on_stream(stream, gdelta_step, state, q, k, v, g, beta, scale, o_out)
     lib = load()
     dt, B, NH, NHV, _, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, None, step=True)
     _need("state", state, (B, NHV, DK, DV), torch.float32, index)
     if o_out is None:
-        o_out = _new(stream, lambda: torch.empty_like(v))
+        o_out = torch.empty_like(v)
     else:
         _need("o_out", o_out, v.shape, q.dtype, index)
-    _check("gdelta_step", _on(index, stream, lambda s: lib.gdelta_step(
+    _check("gdelta_step", _on(index, lambda s: lib.gdelta_step(
         state.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), dt, B, NH, NHV, DK,
         DV, DK ** -0.5 if scale is None else scale, o_out.data_ptr(), s)))
     return o_out
@@ -513,6 +543,8 @@ def gdelta_bwd(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scal
     """gdelta_bwd: gradients of ``sum(do * o) + sum(dstate * final state)`` for the forward pass from
     ``state`` (None: zero; ``dstate`` None: zero).  Returns ``(dq, dk, dv, dg, dbeta, dstate0)``, dstate0
     None without a ``state``; ``out`` may give those six tensors (the last one or None) to write into."""
+    if stream is not None:
+        return _on_stream(stream, gdelta_bwd, q, k, v, g, beta, do, state, dstate, lengths, scale, workspace, out)
     lib = load()
     dt, B, NH, NHV, S, DK, DV, index = _gdelta_inputs(q, k, v, g, beta, lengths)
     _need("do", do, v.shape, q.dtype, index)
@@ -520,15 +552,16 @@ def gdelta_bwd(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scal
         if t is not None:
             _need(name, t, (B, NHV, DK, DV), torch.float32, index)
     if out is None:
-        out = tuple(None if x is None else _new(stream, lambda: torch.empty_like(x)) for x in (q, k, v, g, beta, state))
+        out = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v), torch.empty_like(g),
+               torch.empty_like(beta), None if state is None else torch.empty_like(state))
     else:
         for name, t, x in zip(("dq", "dk", "dv", "dg", "dbeta"), out, (q, k, v, g, beta)):
             _need(name, t, x.shape, x.dtype, index)
         if out[5] is not None:
             _need("dstate0", out[5], (B, NHV, DK, DV), torch.float32, index)
     dq, dk, dv, dg, dbeta, dstate0 = out
-    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, True, stream)
-    _check("gdelta_bwd", _on(index, stream, lambda s: lib.gdelta_bwd(
+    workspace = _gdelta_workspace(workspace, (B, NH, NHV, S, DK, DV, dt), q.device, index, True)
+    _check("gdelta_bwd", _on(index, lambda s: lib.gdelta_bwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _addr(lengths), _addr(state),
         do.data_ptr(), _addr(dstate), dt, B, NH, NHV, S, DK, DV, DK ** -0.5 if scale is None else scale, dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dstate0), workspace.data_ptr(),
@@ -592,17 +625,20 @@ def qknorm_fwd(q, k, q_weight=None, k_weight=None, norm: str = "rms", eps: float
     first RD elements by position * inv_freq (None: no rotation); ``positions`` int32 ``[B, S]``, None for
     0 .. S-1; pairs are (p, p + RD/2), or neighbours with ``interleaved``.
     """
+    if stream is not None:
+        return _on_stream(stream, qknorm_fwd, q, k, q_weight, k_weight, norm, eps, inv_freq, positions, interleaved,
+                          q_out, k_out)
     lib = load()
     dt, B, S, NHQ, NHK, D, RD, kind, index = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
     if q_out is None:
-        q_out = _new(stream, lambda: torch.empty((B, NHQ, S, D), dtype=q.dtype, device=q.device))
+        q_out = torch.empty((B, NHQ, S, D), dtype=q.dtype, device=q.device)
     else:
         _need("q_out", q_out, (B, NHQ, S, D), q.dtype, index)
     if k_out is None:
-        k_out = _new(stream, lambda: torch.empty((B, NHK, S, D), dtype=q.dtype, device=q.device))
+        k_out = torch.empty((B, NHK, S, D), dtype=q.dtype, device=q.device)
     else:
         _need("k_out", k_out, (B, NHK, S, D), q.dtype, index)
-    _check("qknorm_fwd", _on(index, stream, lambda s: lib.qknorm_fwd(
+    _check("qknorm_fwd", _on(index, lambda s: lib.qknorm_fwd(
         q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), _addr(q_weight), _addr(k_weight), _addr(inv_freq),
         _addr(positions), dt, B, S, NHQ, NHK, D, RD, kind, eps, 1 if interleaved else 0, q_out.data_ptr(),
         k_out.data_ptr(), s)))
@@ -615,26 +651,29 @@ def qknorm_bwd(dq_out, dk_out, q, k, q_weight=None, k_weight=None, norm: str = "
     outputs (weight gradients None where the weight is).  ``out`` may give dq ``[B, S, NHQ, D]`` and dk to
     write into, such as slices of a fused projection's gradient (views that share no element), ``workspace`` the
     bytes that qknorm_bwd_workspace_size names."""
+    if stream is not None:
+        return _on_stream(stream, qknorm_bwd, dq_out, dk_out, q, k, q_weight, k_weight, norm, eps, inv_freq,
+                          positions, interleaved, out, workspace)
     lib = load()
     dt, B, S, NHQ, NHK, D, RD, kind, index = _qknorm_inputs(q, k, q_weight, k_weight, norm, inv_freq, positions)
     _need("dq_out", dq_out, (B, NHQ, S, D), q.dtype, index)
     _need("dk_out", dk_out, (B, NHK, S, D), q.dtype, index)
     if out is None:
-        dq = _new(stream, lambda: torch.empty((B, S, NHQ, D), dtype=q.dtype, device=q.device))
-        dk = _new(stream, lambda: torch.empty((B, S, NHK, D), dtype=q.dtype, device=q.device))
+        dq = torch.empty((B, S, NHQ, D), dtype=q.dtype, device=q.device)
+        dk = torch.empty((B, S, NHK, D), dtype=q.dtype, device=q.device)
     else:
         dq, dk = out
         for name, t, x in (("dq", dq, q), ("dk", dk, k)):
             if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != index or (t.numel() and t.stride(3) != 1):
                 raise ValueError("%s must be like its input, the elements of a head contiguous" % name)
-    dwq = None if q_weight is None else _new(stream, lambda: torch.empty_like(q_weight))
-    dwk = None if k_weight is None else _new(stream, lambda: torch.empty_like(k_weight))
+    dwq = None if q_weight is None else torch.empty_like(q_weight)
+    dwk = None if k_weight is None else torch.empty_like(k_weight)
     if workspace is None:
         n = int(lib.qknorm_bwd_workspace_size(B, S, NHQ, NHK, D)) if (dwq is not None or dwk is not None) else 0
-        workspace = _scratch(n, q.device, stream)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     else:
         _need("workspace", workspace, workspace.shape, torch.uint8, index)
-    _check("qknorm_bwd", _on(index, stream, lambda s: lib.qknorm_bwd(
+    _check("qknorm_bwd", _on(index, lambda s: lib.qknorm_bwd(
         dq_out.data_ptr(), dk_out.data_ptr(), q.data_ptr(), _strides(q), k.data_ptr(), _strides(k), _addr(q_weight),
         _addr(k_weight), _addr(inv_freq), _addr(positions), dt, B, S, NHQ, NHK, D, RD, kind, eps,
         1 if interleaved else 0, dq.data_ptr(), _strides(dq), dk.data_ptr(), _strides(dk), _addr(dwq), _addr(dwk),
